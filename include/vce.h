@@ -57,7 +57,9 @@ typedef enum vce_op {
   VCE_OP_LOSS_FWD = 2,
   VCE_OP_LOSS_BWD = 3,
   VCE_OP_SAMPLED_CANDIDATES = 4,
-  VCE_OP_GREEDY_ARGMAX = 5
+  VCE_OP_GREEDY_ARGMAX = 5,
+  VCE_OP_LOGPROB_BWD = 6,
+  VCE_OP_NORM_BWD = 7
 } vce_op;
 
 /*
@@ -334,6 +336,89 @@ vce_status vce_greedy_argmax(const vce_problem* p, const void* h, const void* W,
                              int32_t* dev_status, void* stream);
 
 /*
+ * Token scores (no counterpart on the pages beyond the normaliser of
+ * vce_loss_fwd): for every token t, with l_tv = logit_scale * <h_t, W_v> over
+ * the real classes v < V_real (logit_scale > 0, an inverse temperature),
+ *   lse[t]      = log sum_v exp(l_tv)
+ *   logp[t]     = l_{t,y_t} - lse[t]                   y_t = targets[t]
+ *   entropy[t]  = - sum_v p_tv log p_tv                p_tv = exp(l_tv - lse[t])
+ *   top_ids[t,k], top_logp[t,k], k < n_top: the classes of the n_top largest
+ *                 logits and their log probabilities, largest first, the lower
+ *                 class first between equal logits.
+ * The entropy is summed as log S - U / S with S = sum exp(l - max l) and
+ * U = sum exp(l - max l) (l - max l), in fp32.
+ * An ignored token (targets[t] == ignore_index) has logp = entropy = 0; its lse
+ * and alternatives are those of its row. Any other target outside [0, V_real)
+ * is a data error (VCE_ERR_BAD_INDEX to dev_status) and is treated as ignored.
+ * targets may be NULL when logp is (serving: entropy and alternatives of every
+ * token). logp, entropy and lse may be NULL. 0 <= n_top <= 32 and n_top <=
+ * V_real; top_ids (int64) and top_logp (fp32) are [T, n_top], unused at 0.
+ * A NaN logit is never listed; a row with fewer than n_top listable classes
+ * ends in ids of -1 with NaN. tied_weights is ignored.
+ * Workspace: vce_logprob_workspace_size(p, n_top) bytes (SIZE_MAX if p or n_top
+ * is invalid).
+ */
+size_t vce_logprob_workspace_size(const vce_problem* p, int32_t n_top);
+vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, const int64_t* targets,
+                           float logit_scale, int32_t n_top, float* logp, float* entropy, float* lse,
+                           int64_t* top_ids, float* top_logp, void* ws, size_t ws_bytes, int32_t* dev_status,
+                           void* stream);
+
+/*
+ * Gradient of sum_t (g_logp[t] * logp[t] + g_entropy[t] * entropy[t]):
+ *   G[t,v] = s (g_logp ([v == y] - p) - g_entropy p (log p + entropy)),  s = logit_scale
+ *   dH = G W,   dW = G^T h
+ * lse and entropy must come from vce_logprob_fwd on the same inputs and scale.
+ * g_logp[T] (needs targets) or g_entropy[T] (needs entropy) may be NULL, not
+ * both: a missing one is zero. With targets, a token without a real target has
+ * no gradient: its dH row is 0 (its row of h is not read by the products, so it
+ * may hold anything), and a target that is not ignore_index either is reported
+ * as VCE_ERR_BAD_INDEX. Without targets every token takes part.
+ * dH and dW as in vce_loss_bwd (dH fp32, or bf16 with VCE_FLAG_DH_BF16, added
+ * into with VCE_FLAG_ACCUMULATE_DH; dW added into when tied_weights is 1, else
+ * overwritten with rows [V_real, Vp) zero). dW_dtype is VCE_F32, or VCE_BF16
+ * (bf16 problems, tied_weights 0): the fp32 sum over the tokens rounded once.
+ * As in vce_loss_bwd, bf16 problems form G in bf16 for the two products.
+ * Workspace: vce_workspace_size(p, VCE_OP_LOGPROB_BWD) bytes recommended, any
+ * size from vce_workspace_size_min up accepted.
+ */
+vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, const int64_t* targets,
+                           const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
+                           float logit_scale, void* dH, void* dW, int32_t dW_dtype, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream);
+
+/*
+ * Normalisation of the hidden states in front of the head (no counterpart on
+ * the pages): x[T,H], y[T,H], weight[H] and bias[H] in p->dtype (weight NULL:
+ * ones; bias NULL: zeros), statistics and sums in fp32.
+ *   VCE_NORM_LAYER: mean = mean_i x_i;  VCE_NORM_RMS: mean = 0
+ *   rstd = 1 / sqrt(mean_i (x_i - mean)^2 + eps),   eps >= 0
+ *   y = (x - mean) * rstd * weight + bias, rounded once
+ * mean[T] (0 for RMS) and rstd[T] are kept for the backward; either may be
+ * NULL. y must not overlap x. Uses p->T, H and dtype. No workspace.
+ */
+typedef enum vce_norm_kind { VCE_NORM_LAYER = 0, VCE_NORM_RMS = 1 } vce_norm_kind;
+vce_status vce_norm_fwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* bias,
+                        float eps, void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * Backward of vce_norm_fwd. dy[T,H] is the dH of vce_loss_bwd or
+ * vce_logprob_bwd: fp32, or bf16 with VCE_FLAG_DH_BF16 in p->flags. With xhat =
+ * (x - mean) rstd and g = dy * weight,
+ *   dx      = rstd (g - mean_i(g) - xhat mean_i(g xhat))   in p->dtype
+ *             (without the mean_i(g) term for VCE_NORM_RMS)
+ *   dweight = sum_t dy xhat,   dbias = sum_t dy            fp32 [H]
+ * dx, dweight and dbias may each be NULL (not all three); accumulate = 1 adds
+ * into dweight and dbias, 0 overwrites them. mean may be NULL for VCE_NORM_RMS.
+ * The sums over tokens are taken in an order fixed by the sizes and the device,
+ * so results are bit-identical run to run. dx must not overlap x or dy.
+ * Workspace: vce_workspace_size(p, VCE_OP_NORM_BWD) bytes.
+ */
+vce_status vce_norm_bwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* dy,
+                        const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                        int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Hashed n-gram input embeddings ["Sampled Softmax with Over-Tokenized
  * Transformer", Setup and its loss listing: each input token's embedding gains
  * the hashed 2-gram and 3-gram embeddings that end at it].
@@ -481,7 +566,9 @@ typedef enum vce_kernel_kind {
   VCE_K_DH_REDUCE = 14, VCE_K_SAMPLED_CAND = 15, VCE_K_SAMPLED_SCATTER = 16,
   VCE_K_TC_ARGMAX = 17, VCE_K_ARGMAX_MERGE = 18, VCE_K_SIMT_ARGMAX = 19,
   VCE_K_NGRAM_HASH = 20, VCE_K_NGRAM_FWD = 21, VCE_K_EMBED_HDR = 22, VCE_K_DH_BF16 = 23,
-  VCE_K_EMBED_SORT_CLUSTER = 24
+  VCE_K_EMBED_SORT_CLUSTER = 24, VCE_K_TC_LOGITS = 25, VCE_K_SCORE_ROWS = 26, VCE_K_TC_SCORE_GRAD = 27,
+  VCE_K_SIMT_LOGITS = 28, VCE_K_SIMT_SCORE_GRAD = 29, VCE_K_MASK_ROWS = 30, VCE_K_NORM_FWD = 31,
+  VCE_K_NORM_BWD = 32, VCE_K_NORM_SUM = 33
 } vce_kernel_kind;
 uint64_t vce_launch_count(void);
 vce_status vce_profile_begin(int32_t capacity, void* stream);

@@ -23,6 +23,9 @@ VCE_FLAG_DH_BF16 = 2
 VCE_OP_EMBED_FWD, VCE_OP_EMBED_BWD, VCE_OP_LOSS_FWD, VCE_OP_LOSS_BWD = 0, 1, 2, 3
 VCE_OP_SAMPLED_CANDIDATES = 4
 VCE_OP_GREEDY_ARGMAX = 5
+VCE_OP_LOGPROB_BWD = 6
+VCE_OP_NORM_BWD = 7
+VCE_NORM_LAYER, VCE_NORM_RMS = 0, 1
 SIZE_MAX = (1 << 64) - 1
 
 
@@ -101,6 +104,20 @@ def lib():
                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                        c_void_p, c_size_t, c_void_p, c_void_p]
         L.vce_sampled_loss.restype = c_int32
+        L.vce_logprob_workspace_size.argtypes = [P, c_int32]
+        L.vce_logprob_workspace_size.restype = c_size_t
+        L.vce_logprob_fwd.argtypes = [P, c_void_p, c_void_p, c_void_p, c_float, c_int32, c_void_p, c_void_p, c_void_p,
+                                      c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]
+        L.vce_logprob_fwd.restype = c_int32
+        L.vce_logprob_bwd.argtypes = [P, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_float,
+                                      c_void_p, c_void_p, c_int32, c_void_p, c_size_t, c_void_p, c_void_p]
+        L.vce_logprob_bwd.restype = c_int32
+        L.vce_norm_fwd.argtypes = [P, c_int32, c_void_p, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_void_p,
+                                   c_void_p]
+        L.vce_norm_fwd.restype = c_int32
+        L.vce_norm_bwd.argtypes = [P, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_int32, c_void_p, c_size_t, c_void_p]
+        L.vce_norm_bwd.restype = c_int32
         L.vce_status_str.argtypes = [c_int32]
         L.vce_status_str.restype = ctypes.c_char_p
         L.vce_embed_bwd_chunk.argtypes = []
@@ -243,6 +260,87 @@ def vce_greedy_argmax(p, h, W, argmax, max_logit=None, owner=None, ws=None, ws_b
                                    _ptr(ws), nb, _ptr(dev_status), _stream(stream)), "vce_greedy_argmax")
 
 
+def vce_logprob_workspace_size(p: VceProblem, n_top: int) -> int:
+    return int(lib().vce_logprob_workspace_size(ctypes.byref(p), int(n_top)))
+
+
+def _arg(x, name: str, dtype, shape, optional=False) -> Optional[int]:
+    """Device pointer of a contiguous CUDA tensor of exactly this element type and shape."""
+    if x is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if not x.is_cuda or x.dtype != dtype or tuple(x.shape) != shape or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtype} {list(shape)}, got {x.dtype} "
+                         f"{list(x.shape)} with strides {list(x.stride())} on {x.device}")
+    return x.data_ptr()
+
+
+def _elem(p: VceProblem):
+    import torch
+    return torch.bfloat16 if p.dtype == VCE_BF16 else torch.float32
+
+
+def _dh_elem(p: VceProblem):
+    import torch
+    return torch.bfloat16 if p.flags & VCE_FLAG_DH_BF16 else torch.float32
+
+
+def vce_logprob_fwd(p, h, W, targets, logp=None, entropy=None, lse=None, top_ids=None, top_logp=None, logit_scale=1.0,
+                    ws=None, ws_bytes=None, dev_status=None, stream=None) -> None:
+    """n_top is the second size of top_ids [T, n_top] (0 without it)."""
+    import torch
+    nb = (ws.numel() * ws.element_size() if ws is not None else 0) if ws_bytes is None else ws_bytes
+    T, e, f32, i64 = p.T, _elem(p), torch.float32, torch.int64
+    K = 0 if top_ids is None else int(top_ids.shape[-1])
+    top_shape = (T, K)
+    _check(lib().vce_logprob_fwd(ctypes.byref(p), _arg(h, "h", e, (T, p.H)), _arg(W, "W", e, (p.Vp, p.H)),
+                                 _arg(targets, "targets", i64, (T,), True), float(logit_scale), K,
+                                 _arg(logp, "logp", f32, (T,), True), _arg(entropy, "entropy", f32, (T,), True),
+                                 _arg(lse, "lse", f32, (T,), True), _arg(top_ids, "top_ids", i64, top_shape, True),
+                                 _arg(top_logp, "top_logp", f32, top_shape, K == 0), _ptr(ws), nb, _ptr(dev_status),
+                                 _stream(stream)), "vce_logprob_fwd")
+
+
+def vce_logprob_bwd(p, h, W, targets, lse, entropy, g_logp, g_entropy, dH, dW, ws, logit_scale=1.0, ws_bytes=None,
+                    dev_status=None, stream=None) -> None:
+    """dW's element type (fp32, or bf16 on an untied bf16 problem) is that of the tensor."""
+    import torch
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    T, e, f32 = p.T, _elem(p), torch.float32
+    dw_bf16 = dW is not None and dW.dtype == torch.bfloat16
+    _check(lib().vce_logprob_bwd(ctypes.byref(p), _arg(h, "h", e, (T, p.H)), _arg(W, "W", e, (p.Vp, p.H)),
+                                 _arg(targets, "targets", torch.int64, (T,), True), _arg(lse, "lse", f32, (T,)),
+                                 _arg(entropy, "entropy", f32, (T,), True), _arg(g_logp, "g_logp", f32, (T,), True),
+                                 _arg(g_entropy, "g_entropy", f32, (T,), True), float(logit_scale),
+                                 _arg(dH, "dH", _dh_elem(p), (T, p.H)),
+                                 _arg(dW, "dW", torch.bfloat16 if dw_bf16 else f32, (p.Vp, p.H)),
+                                 VCE_BF16 if dw_bf16 else VCE_F32, _ptr(ws), nb, _ptr(dev_status), _stream(stream)),
+           "vce_logprob_bwd")
+
+
+def vce_norm_fwd(p, x, weight, bias, y, mean=None, rstd=None, eps=1e-5, kind=VCE_NORM_LAYER, stream=None) -> None:
+    import torch
+    T, H, e, f32 = p.T, p.H, _elem(p), torch.float32
+    _check(lib().vce_norm_fwd(ctypes.byref(p), int(kind), _arg(x, "x", e, (T, H)),
+                              _arg(weight, "weight", e, (H,), True), _arg(bias, "bias", e, (H,), True), float(eps),
+                              _arg(y, "y", e, (T, H)), _arg(mean, "mean", f32, (T,), True),
+                              _arg(rstd, "rstd", f32, (T,), True), _stream(stream)), "vce_norm_fwd")
+
+
+def vce_norm_bwd(p, x, weight, dy, mean, rstd, dx, dweight, dbias, ws, kind=VCE_NORM_LAYER, accumulate=False,
+                 ws_bytes=None, stream=None) -> None:
+    import torch
+    nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
+    T, H, e, f32 = p.T, p.H, _elem(p), torch.float32
+    _check(lib().vce_norm_bwd(ctypes.byref(p), int(kind), _arg(x, "x", e, (T, H)),
+                              _arg(weight, "weight", e, (H,), True), _arg(dy, "dy", _dh_elem(p), (T, H)),
+                              _arg(mean, "mean", f32, (T,), True), _arg(rstd, "rstd", f32, (T,)),
+                              _arg(dx, "dx", e, (T, H), True), _arg(dweight, "dweight", f32, (H,), True),
+                              _arg(dbias, "dbias", f32, (H,), True), int(bool(accumulate)), _ptr(ws), nb,
+                              _stream(stream)), "vce_norm_bwd")
+
+
 def vce_ngram_hash(ids, n, V, M, out, seq_len=0, stream=None) -> None:
     _check(lib().vce_ngram_hash(_ptr(ids), int(ids.numel()), int(n), int(V), int(M), int(seq_len), _ptr(out),
                                 _stream(stream)), "vce_ngram_hash")
@@ -299,7 +397,8 @@ def vce_wait_selftest(limit_ns: int, dev_status, stream=None) -> None:
 KERNEL_KINDS = ["embed_gather", "embed_sort", "embed_reduce", "tc_fwd", "tc_grad", "tc_dh", "tc_dw",
                 "merge", "loss_mean", "count_valid", "simt_fwd", "simt_grad", "sgemm", "wait_selftest",
                 "dh_reduce", "sampled_cand", "sampled_scatter", "tc_argmax", "argmax_merge", "simt_argmax",
-                "ngram_hash", "ngram_fwd", "embed_hdr", "dh_bf16", "embed_sort_cluster"]
+                "ngram_hash", "ngram_fwd", "embed_hdr", "dh_bf16", "embed_sort_cluster", "tc_logits", "score_rows",
+                "tc_score_grad", "simt_logits", "simt_score_grad", "mask_rows", "norm_fwd", "norm_bwd", "norm_sum"]
 
 
 def vce_launch_count() -> int:

@@ -75,6 +75,16 @@ inline ProbDev prob_dev(const vce_problem& p) {
                  static_cast<int32_t>(p.V_real), p.S, p.ignore_index};
 }
 
+// What the token scores' gradient needs of each token besides h and W: the
+// forward's lse and entropy and the upstream gradients (either may be null).
+struct ScoreGrad {
+  const float* lse;
+  const float* entropy;
+  const float* g_logp;
+  const float* g_entropy;
+  float scale;   // logits are scale * <h, W>
+};
+
 // Host-side argument rules shared by every entry point that takes a problem
 // (shapes, flags, dtype, the ignore value, 32-bit work-item numbering).
 vce_status check_problem(const vce_problem* p);
@@ -179,6 +189,10 @@ cudaError_t launch_simt_argmax(const ProbDev& pd, const UnitGrid& ug, const floa
 cudaError_t launch_simt_grad(const ProbDev& pd, const float* h, const float* W, const int64_t* targets,
                              const float* lse, const int32_t* n_valid, float g, int v0, int vc, float* G,
                              cudaStream_t st);
+cudaError_t launch_simt_logits(const ProbDev& pd, const float* h, const float* W, float* Z, int64_t ldz,
+                               cudaStream_t st);
+cudaError_t launch_simt_score_grad(const ProbDev& pd, const float* h, const float* W, const int64_t* targets,
+                                   const ScoreGrad& sg, int v0, int vc, float* G, cudaStream_t st);
 // C[M,N] = beta*C + sum_k A(m,k) B(k,n), A(m,k) = A[m*sam + k*sak], B(k,n) = B[k*sbk + n*sbn],
 // C row-major with leading dimension ldc. beta is 0 or 1.
 cudaError_t launch_sgemm(int M, int N, int K, const float* A, int64_t sam, int64_t sak, const float* B,
@@ -192,8 +206,12 @@ cudaError_t launch_tc_argmax(const vce_problem& p, const UnitGrid& ug, const voi
                              int32_t* status, cudaStream_t st);
 cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void* W, const int64_t* targets,
                                 const float* lse, float g, int v0, int vc_act,
-                                void* G, int g_ld, float* dH, bool dH_accumulate, float* dW, bool dW_accumulate,
-                                int32_t* dh_flags, int dh_parts, int32_t* status, cudaStream_t st);
+                                void* G, int g_ld, float* dH, bool dH_accumulate, void* dW, bool dW_accumulate,
+                                int32_t* dh_flags, int dh_parts, int32_t* status, cudaStream_t st,
+                                const ScoreGrad* sg = nullptr, bool dW_bf16 = false);
+// Z[T, V_real] (row stride ldz, a multiple of 4) = h W^T in fp32.
+cudaError_t launch_tc_logits(const vce_problem& p, const void* h, const void* W, float* Z, int64_t ldz,
+                             int32_t* status, cudaStream_t st);
 // Number of K parts for the dH GEMM of one column chunk (fills the waves of
 // the persistent grid); at most kMaxDhParts.
 constexpr int kMaxDhParts = 8;
@@ -213,6 +231,25 @@ cudaError_t launch_ngram_hash_pair(const int64_t* ids, int64_t T, int64_t V, int
 cudaError_t launch_ngram_embed_fwd(const vce_problem& p, const int64_t* ids, const void* W, const void* T2,
                                    int64_t M2, const void* T3, int64_t M3, int64_t seq_len, void* E,
                                    cudaStream_t st);
+
+// Token scores (score.cu): the longest list of alternatives, and the launchers.
+constexpr int kMaxTop = 32;
+// Scores of `rows` rows of logits, token t0 + row each; see vce_logprob_fwd.
+cudaError_t launch_score_rows(const float* Z, int64_t ldz, int64_t rows, int V, int64_t t0, const int64_t* targets,
+                              int64_t ignore_index, float scale, int K, float* logp, float* entropy, float* lse,
+                              int64_t* top_ids, float* top_logp, int32_t* status, cudaStream_t st);
+// out = h with the rows of tokens without a real target set to zero.
+cudaError_t launch_mask_rows(const void* h, const int64_t* targets, int64_t T, int V, int64_t ignore_index,
+                             int64_t row_bytes, void* out, int32_t* status, cudaStream_t st);
+
+// Layer and RMS normalisation (norm.cu).
+int norm_parts(const vce_problem& p);
+size_t norm_ws_bytes(const vce_problem& p);
+cudaError_t launch_norm_fwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* b, float eps,
+                            void* y, float* mean, float* rstd, cudaStream_t st);
+cudaError_t launch_norm_bwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* dy, bool dy_bf16,
+                            const float* mean, const float* rstd, void* dx, float* dw, float* db, bool accumulate,
+                            void* ws, cudaStream_t st);
 
 // Sampled-softmax candidate list.
 size_t sampled_ws_bytes(const vce_problem& p);

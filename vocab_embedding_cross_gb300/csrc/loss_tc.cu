@@ -11,6 +11,11 @@
 //         G = (exp(z - lse) - [v == y]) * g / N_valid in bf16 and stores it.
 //   DH    dH (+)= G W      (A = G K-major, B = W rows as an MN-major operand)
 //   DW    dW (+)= G^T h    (A = G^T and B = h, both MN-major operands)
+// and the token scores' (log probabilities, entropy, top alternatives):
+//   LOGITS z = h W^T stored in fp32
+//   SGRAD  z recomputed; the epilogue forms the scores' gradient with respect
+//          to the logits in bf16 (score_grad below)
+//   DWB    DW with a bf16 result
 //
 // Two CTAs on two SMs form a cluster and share each MMA (tcgen05 cta_group::2,
 // M = 256, N = 256, K = 16): each CTA loads 128 rows of A and half of B's N
@@ -55,15 +60,32 @@ constexpr uint32_t kStagingPerWarp = 4096;       // one 32-row x 128-B TMA store
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum Mode : int { MODE_FWD = 0, MODE_GRAD = 1, MODE_DH = 2, MODE_DW = 3, MODE_ARGMAX = 4 };
+enum Mode : int {
+  MODE_FWD = 0, MODE_GRAD = 1, MODE_DH = 2, MODE_DW = 3, MODE_ARGMAX = 4, MODE_LOGITS = 5, MODE_SGRAD = 6, MODE_DWB = 7
+};
 // FWD and ARGMAX share the logit GEMM and its work items; they differ in the epilogue.
 template <int MODE>
 constexpr bool kFwdLike = MODE == MODE_FWD || MODE == MODE_ARGMAX;
+// GRAD, SGRAD and LOGITS work on single 256 x 256 logit tiles of one column chunk.
+template <int MODE>
+constexpr bool kTileLike = MODE == MODE_GRAD || MODE == MODE_SGRAD || MODE == MODE_LOGITS;
+// GRAD and SGRAD store a bf16 gradient tile and precede a DH launch.
+template <int MODE>
+constexpr bool kGradLike = MODE == MODE_GRAD || MODE == MODE_SGRAD;
+template <int MODE>
+constexpr bool kDwLike = MODE == MODE_DW || MODE == MODE_DWB;
+constexpr int kernel_kind(int mode) {
+  return mode == MODE_ARGMAX   ? VCE_K_TC_ARGMAX
+         : mode == MODE_LOGITS ? VCE_K_TC_LOGITS
+         : mode == MODE_SGRAD  ? VCE_K_TC_SCORE_GRAD
+         : mode == MODE_DWB    ? VCE_K_TC_DW
+                               : VCE_K_TC_FWD + mode;
+}
 
 template <int MODE>
 struct Traits {
-  static constexpr uint32_t a_mn = (MODE == MODE_DW) ? 1u : 0u;
-  static constexpr uint32_t b_mn = (MODE == MODE_DH || MODE == MODE_DW) ? 1u : 0u;
+  static constexpr uint32_t a_mn = kDwLike<MODE> ? 1u : 0u;
+  static constexpr uint32_t b_mn = (MODE == MODE_DH || kDwLike<MODE>) ? 1u : 0u;
   static constexpr bool staging = !kFwdLike<MODE>;
   static constexpr int stages = 6;
   static constexpr uint32_t idesc = idesc_bf16_f32(BMP, BN, a_mn, b_mn);
@@ -101,6 +123,7 @@ struct TcArgs {
   int32_t* status;
   uint64_t limit_ns;
   int32_t* merge_ctr;   // FWD: the merge's block counter, zeroed here for the merge that follows
+  ScoreGrad sg;         // SGRAD: what the forward scores left and their upstream gradients
 };
 
 // Items of the forward-like modes and of GRAD are (token block m, column
@@ -160,7 +183,7 @@ __device__ __forceinline__ TileCoord tile_coord(const TcArgs& a, int item, int t
     const UnitSpan us = unit_span(a, mc.c);
     c.am = mc.m * BMP + rank * BM;
     c.bn = static_cast<int32_t>(us.vb + static_cast<int64_t>(tt) * BN) + rank * BNH;
-  } else if constexpr (MODE == MODE_GRAD) {
+  } else if constexpr (kTileLike<MODE>) {
     const MC mc = item_mc(item, a.gm, a.n_mblk, a.n_cols);
     c.am = mc.m * BMP + rank * BM;
     c.bn = a.v0 + mc.c * BN + rank * BNH;
@@ -195,7 +218,7 @@ template <int MODE>
 __device__ __forceinline__ void issue_loads(const TcArgs& a, const CUtensorMap* mA, const CUtensorMap* mB,
                                             uint32_t sA, uint32_t sB, uint32_t bar, TileCoord c, int kb) {
   const int k0 = kb * BK;
-  if constexpr (kFwdLike<MODE> || MODE == MODE_GRAD) {
+  if constexpr (kFwdLike<MODE> || kTileLike<MODE>) {
     tma_load_2d_pair(sA, mA, bar, k0, c.am);
     tma_load_2d_pair(sB, mB, bar, k0, c.bn);
   } else if constexpr (MODE == MODE_DH) {
@@ -236,6 +259,32 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_u32(bar))
                : "memory");
+}
+
+// One token's constants of the score gradient. With l = s z the scaled logit and
+// logp = l - lse, the loss g_logp * logp_y + g_entropy * entropy has
+//   dL/dz_v = s (g_logp ([v == y] - p_v) - g_entropy p_v (logp_v + entropy))
+//           = p_v (c0 + c1 (logp_v + entropy)) + [v == y] hit.
+// logp is one rounding of s z - lse before anything else is added, so that it
+// keeps its relative precision in peaked rows, where it is near 0.
+struct ScoreGradRow {
+  float s, lse, ent, c0, c1, hit;
+};
+__device__ __forceinline__ ScoreGradRow score_grad_row(const ScoreGrad& g, int t) {
+  ScoreGradRow r;
+  const float gl = g.g_logp ? g.g_logp[t] : 0.0f;
+  const float ge = g.g_entropy ? g.g_entropy[t] : 0.0f;
+  r.s = g.scale;
+  r.lse = g.lse[t];
+  r.ent = g.g_entropy ? g.entropy[t] : 0.0f;
+  r.hit = g.scale * gl;
+  r.c0 = -r.hit;
+  r.c1 = -g.scale * ge;
+  return r;
+}
+__device__ __forceinline__ float score_grad(const ScoreGradRow& r, float z) {
+  const float lp = fmaf(z, r.s, -r.lse);
+  return ex2_approx(lp * kLog2e) * fmaf(lp + r.ent, r.c1, r.c0);
 }
 
 template <int MODE>
@@ -302,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if constexpr (MODE == MODE_FWD) {
     if (a.merge_ctr && blockIdx.x == 0 && threadIdx.x == 0) *a.merge_ctr = 0;
   }
-  if constexpr (MODE == MODE_GRAD) {   // the next DH launch's part counters start at zero
+  if constexpr (kGradLike<MODE>) {   // the next DH launch's part counters start at zero
     for (int i = static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x); i < a.n_dh_flags;
          i += static_cast<int>(gridDim.x * blockDim.x))
       a.dh_flags[i] = 0;
@@ -468,7 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
     };
     // One 32-row x 128-byte TMA store (or reduce-add) from this warp's staging box.
-    bool add_out = MODE != MODE_GRAD && a.accumulate;
+    bool add_out = !kTileLike<MODE> && a.accumulate;
     auto store_box = [&](const uint32_t (&w)[32], int col, int row) {
       if (lane == 0) bulk_wait_read<0>();
       __syncwarp();
@@ -672,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++items_done;
       } else {
         int m_blk, n_blk, row0, col0, part = 0;
-        if constexpr (MODE == MODE_GRAD) {
+        if constexpr (kTileLike<MODE>) {
           const MC mc = item_mc(item, a.gm, a.n_mblk, a.n_cols);
           m_blk = mc.m;
           n_blk = mc.c;
@@ -682,7 +731,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           n_blk = item % a.n_nblk;
           m_blk = (item / a.n_nblk) % a.n_mblk;
           part = (item / a.n_nblk) / a.n_mblk;   // DH: this item's K part
-          row0 = (MODE == MODE_DW ? a.out_row0 : 0) + m_blk * BMP + static_cast<int>(rank) * BM;
+          row0 = (kDwLike<MODE> ? a.out_row0 : 0) + m_blk * BMP + static_cast<int>(rank) * BM;
           col0 = n_blk * BN + half * 128;
         }
         const int orow = row0 + q * 32;
@@ -747,6 +796,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (j == jy) g0 -= scale;
               if (j + 1 == jy) g1 -= scale;
               w[j / 2] = pack_bf16x2(g0, g1);
+            }
+            store_box(w, col0 + bb * 64, orow);
+          }
+        } else if constexpr (MODE == MODE_SGRAD) {
+          const int t = m_blk * BMP + static_cast<int>(rank) * BM + r;
+          int64_t y = -1;
+          bool row_ok = false;
+          ScoreGradRow sr{};
+          if (t < a.pd.T) {
+            y = a.targets ? a.targets[t] : -1;
+            row_ok = a.targets ? (y >= 0 && y < a.pd.V_real) : true;
+            sr = score_grad_row(a.sg, t);
+          }
+          const int64_t vt0 = static_cast<int64_t>(a.v0) + col0;
+#pragma unroll 1
+          for (int bb = 0; bb < 2; ++bb) {
+            uint32_t x0[32], x1[32], w[32];
+            tmem_ld_32x32b_x32(ta + bb * 64, x0);
+            tmem_ld_32x32b_x32(ta + bb * 64 + 32, x1);
+            tmem_ld_wait();
+            reg_fence(x0);
+            reg_fence(x1);
+            if (bb == 1) release(acc);
+            const int64_t vc0 = vt0 + bb * 64;
+            // real columns and the target's column of the chunk, as in GRAD
+            const int64_t nv64 = row_ok ? a.pd.V_real - vc0 : 0;
+            const int nval = nv64 >= 64 ? 64 : (nv64 <= 0 ? 0 : static_cast<int>(nv64));
+            const int64_t jy64 = y - vc0;
+            const int jy = (row_ok && jy64 >= 0 && jy64 < 64) ? static_cast<int>(jy64) : -1;
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+              const uint32_t xa = j < 32 ? x0[j] : x1[j - 32];
+              const uint32_t xb = j < 32 ? x0[j + 1] : x1[j - 31];
+              float g0 = 0.0f, g1 = 0.0f;
+              if (j < nval) g0 = score_grad(sr, __uint_as_float(xa));
+              if (j + 1 < nval) g1 = score_grad(sr, __uint_as_float(xb));
+              if (j == jy) g0 += sr.hit;
+              if (j + 1 == jy) g1 += sr.hit;
+              w[j / 2] = pack_bf16x2(g0, g1);
+            }
+            store_box(w, col0 + bb * 64, orow);
+          }
+        } else if constexpr (MODE == MODE_DWB) {
+          // The whole sum over the tokens is in this one accumulator: rounded
+          // to bf16 once, 64 columns to a 128-byte row of the store box.
+#pragma unroll 1
+          for (int bb = 0; bb < 2; ++bb) {
+            uint32_t x0[32], x1[32], w[32];
+            tmem_ld_32x32b_x32(ta + bb * 64, x0);
+            tmem_ld_32x32b_x32(ta + bb * 64 + 32, x1);
+            tmem_ld_wait();
+            reg_fence(x0);
+            reg_fence(x1);
+            if (bb == 1) release(acc);
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+              const uint32_t xa = j < 32 ? x0[j] : x1[j - 32];
+              const uint32_t xb = j < 32 ? x0[j + 1] : x1[j - 31];
+              w[j / 2] = pack_bf16x2(__uint_as_float(xa), __uint_as_float(xb));
             }
             store_box(w, col0 + bb * 64, orow);
           }
@@ -851,7 +959,7 @@ cudaError_t launch_mode(const CUtensorMap& mA, const CUtensorMap& mB, const CUte
   const int clusters = a.n_items < mc ? a.n_items : mc;
   const cudaError_t e = launch_dependent(tc_loss_kernel<MODE>, dim3(2 * clusters), dim3(kThreads), smem_bytes<MODE>(),
                                          st, mA, mB, mO, a);
-  note_launch(MODE == MODE_ARGMAX ? VCE_K_TC_ARGMAX : VCE_K_TC_FWD + MODE, st);
+  note_launch(kernel_kind(MODE), st);
   return e;
 }
 
@@ -1006,10 +1114,28 @@ cudaError_t launch_tc_argmax(const vce_problem& p, const UnitGrid& ug, const voi
   return launch_mode<MODE_ARGMAX>(mh, mw, mh, a, st);
 }
 
+cudaError_t launch_tc_logits(const vce_problem& p, const void* h, const void* W, float* Z, int64_t ldz,
+                             int32_t* status, cudaStream_t st) {
+  CUtensorMap mh, mw, mz;
+  if (!make_tmap_2d(&mh, h, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.T, p.H, 64, BM, true) ||
+      !make_tmap_2d(&mw, W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.V_real, p.H, 64, BNH, true) ||
+      !make_tmap_2d(&mz, Z, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.V_real, p.T, ldz, 32, 32, true))
+    return cudaErrorInvalidValue;
+  TcArgs a = base_args(p, nullptr, status);
+  a.n_mblk = static_cast<int>(ceil_div(p.T, BMP));
+  a.n_nblk = static_cast<int>(ceil_div(p.V_real, BN));
+  a.n_items = a.n_mblk * a.n_nblk;
+  a.gm = tc_group_mblk(p);
+  a.n_cols = a.n_nblk;
+  a.num_kb = static_cast<int>(ceil_div(p.H, BK));
+  return launch_mode<MODE_LOGITS>(mh, mw, mz, a, st);
+}
+
 cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void* W, const int64_t* targets,
                                 const float* lse, float g, int v0, int vc_act, void* G,
-                                int g_ld, float* dH, bool dH_accumulate, float* dW, bool dW_accumulate,
-                                int32_t* dh_flags, int dh_parts, int32_t* status, cudaStream_t st) {
+                                int g_ld, float* dH, bool dH_accumulate, void* dW, bool dW_accumulate,
+                                int32_t* dh_flags, int dh_parts, int32_t* status, cudaStream_t st,
+                                const ScoreGrad* sg, bool dW_bf16) {
   const int parts = dh_flags ? dh_parts : 1;
   const int n_flags = static_cast<int>(ceil_div(p.T, BMP) * ceil_div(p.H, BN)) * 2 * kEpiWarps;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1035,7 +1161,13 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     a.vc = vc_act;
     a.dh_flags = parts > 1 ? dh_flags : nullptr;
     a.n_dh_flags = parts > 1 ? n_flags : 0;
-    if ((e = launch_mode<MODE_GRAD>(mh, mw, mg, a, st)) != cudaSuccess) return e;
+    if (sg) {
+      a.sg = *sg;
+      e = launch_mode<MODE_SGRAD>(mh, mw, mg, a, st);
+    } else {
+      e = launch_mode<MODE_GRAD>(mh, mw, mg, a, st);
+    }
+    if (e != cudaSuccess) return e;
   }
   // DH: dH (+)= G[:, 0:vc_act] W[v0:v0+vc_act, :]. With dh_parts > 1 the K
   // range is cut into parts; each part's tile is added into dH after the part
@@ -1064,7 +1196,8 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     CUtensorMap mg, mh, mo;
     if (!make_tmap_2d(&mg, G, BF, 2, vc_act, p.T, g_ld, 64, 64, true) ||
         !make_tmap_2d(&mh, h, BF, 2, p.H, p.T, p.H, 64, 64, true) ||
-        !make_tmap_2d(&mo, dW, F32, 4, p.H, static_cast<uint64_t>(v0) + vc_act, p.H, 32, 32, true))
+        !make_tmap_2d(&mo, dW, dW_bf16 ? BF : F32, dW_bf16 ? 2 : 4, p.H, static_cast<uint64_t>(v0) + vc_act, p.H,
+                      dW_bf16 ? 64 : 32, 32, true))
       return cudaErrorInvalidValue;
     TcArgs a = base_args(p, targets, status);
     a.n_mblk = static_cast<int>(ceil_div(vc_act, BMP));
@@ -1073,7 +1206,8 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     a.num_kb = static_cast<int>(ceil_div(p.T, BK));
     a.out_row0 = v0;
     a.accumulate = dW_accumulate ? 1 : 0;
-    if ((e = launch_mode<MODE_DW>(mg, mh, mo, a, st)) != cudaSuccess) return e;
+    e = dW_bf16 ? launch_mode<MODE_DWB>(mg, mh, mo, a, st) : launch_mode<MODE_DW>(mg, mh, mo, a, st);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -199,6 +200,23 @@ size_t dh_acc_bytes(const vce_problem& p) {
   return align_up(static_cast<size_t>(p.T) * static_cast<size_t>(p.H) * sizeof(float), kWsAlign);
 }
 
+// ----- token scores -----
+// Tokens whose logits are in the workspace at one time: at most 512 MiB of
+// them, in whole token blocks of the tensor-core kernels.
+int64_t score_rows_per_pass(const vce_problem& p) {
+  const int64_t cap = (int64_t(512) << 20) / (p.Vp * 4);
+  int64_t r = cap >= 256 ? cap / 256 * 256 : cap;
+  if (r < 1) r = 1;
+  return r < p.T ? r : p.T;
+}
+size_t score_ws_bytes(const vce_problem& p) {
+  return kWsAlign + align_up(static_cast<size_t>(score_rows_per_pass(p)) * static_cast<size_t>(p.Vp) * 4, kWsAlign);
+}
+// The backward's copy of h without the rows of ignored tokens.
+size_t masked_h_bytes(const vce_problem& p) {
+  return align_up(static_cast<size_t>(p.T) * static_cast<size_t>(p.H) * g_esize(p), kWsAlign);
+}
+
 // ----- sampled softmax: the sub-problems and the workspace layout -----
 // Candidate table: P rows, padded to a multiple of 64 for the loss kernels.
 int64_t cand_rows(int64_t P) { return ceil_div(P, 64) * 64; }
@@ -318,6 +336,9 @@ size_t vce_workspace_size(const vce_problem* p, int32_t op) {
       return dh_acc_bytes(*p) + bwd_bytes_for(*p, bwd_recommended_cols(*p)) + dh_flag_bytes(*p);
     case VCE_OP_SAMPLED_CANDIDATES: return sampled_ws_bytes(*p);
     case VCE_OP_GREEDY_ARGMAX: return argmax_ws_bytes(*p);
+    case VCE_OP_LOGPROB_BWD:
+      return dh_acc_bytes(*p) + masked_h_bytes(*p) + bwd_bytes_for(*p, bwd_recommended_cols(*p)) + dh_flag_bytes(*p);
+    case VCE_OP_NORM_BWD: return norm_ws_bytes(*p);
   }
   return SIZE_MAX;
 }
@@ -325,6 +346,8 @@ size_t vce_workspace_size(const vce_problem* p, int32_t op) {
 size_t vce_workspace_size_min(const vce_problem* p, int32_t op) {
   if (check_problem(p) != VCE_OK) return SIZE_MAX;
   if (op == VCE_OP_LOSS_BWD) return dh_acc_bytes(*p) + bwd_bytes_for(*p, p->T == 0 ? 0 : 256);
+  if (op == VCE_OP_LOGPROB_BWD)
+    return dh_acc_bytes(*p) + masked_h_bytes(*p) + bwd_bytes_for(*p, p->T == 0 ? 0 : 256);
   return vce_workspace_size(p, op);
 }
 
@@ -593,6 +616,173 @@ vce_status vce_greedy_argmax(const vce_problem* p, const void* h, const void* W,
                                            st);
   if (e != cudaSuccess) return cuda_status(e);
   return cuda_status(launch_argmax_merge(pd, ug, part, argmax, max_logit, owner, st));
+}
+
+size_t vce_logprob_workspace_size(const vce_problem* p, int32_t n_top) {
+  if (check_problem(p) != VCE_OK || n_top < 0 || n_top > kMaxTop || n_top > p->V_real) return SIZE_MAX;
+  return score_ws_bytes(*p);
+}
+
+vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, const int64_t* targets,
+                           float logit_scale, int32_t n_top, float* logp, float* entropy, float* lse,
+                           int64_t* top_ids, float* top_logp, void* ws, size_t ws_bytes, int32_t* dev_status,
+                           void* stream) {
+  vce_status s = check_problem(p);
+  if (s != VCE_OK) return s;
+  if (n_top < 0 || n_top > kMaxTop || n_top > p->V_real) return VCE_ERR_ARG;
+  if (!(logit_scale > 0.0f) || !std::isfinite(logit_scale)) return VCE_ERR_ARG;
+  if (p->T == 0) return VCE_OK;
+  if (!h || !W || (logp && !targets) || (n_top > 0 && (!top_ids || !top_logp))) return VCE_ERR_ARG;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+      !aligned(lse, 4) || !aligned(top_ids, 8) || !aligned(top_logp, 4))
+    return VCE_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, kWsAlign) || ws_bytes < score_ws_bytes(*p)) return VCE_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  char* b = static_cast<char*>(ws);
+  int32_t* status = dev_status;
+  if (!status) {
+    status = reinterpret_cast<int32_t*>(b);
+    if (cudaError_t me = cudaMemsetAsync(status, 0, sizeof(int32_t), st)) return cuda_status(me);
+  }
+  float* Z = reinterpret_cast<float*>(b + kWsAlign);
+  const int64_t rows = score_rows_per_pass(*p);
+  for (int64_t t0 = 0; t0 < p->T; t0 += rows) {
+    vce_problem q = *p;
+    q.T = p->T - t0 < rows ? p->T - t0 : rows;
+    const char* hr = static_cast<const char*>(h) + static_cast<size_t>(t0) * p->H * esize_of(*p);
+    cudaError_t e = p->dtype == VCE_BF16
+                        ? launch_tc_logits(q, hr, W, Z, p->Vp, status, st)
+                        : launch_simt_logits(prob_dev(q), reinterpret_cast<const float*>(hr),
+                                             static_cast<const float*>(W), Z, p->Vp, st);
+    if (e == cudaSuccess)
+      e = launch_score_rows(Z, p->Vp, q.T, static_cast<int>(p->V_real), t0, targets, p->ignore_index, logit_scale,
+                            n_top, logp, entropy, lse, top_ids, top_logp, status, st);
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  return VCE_OK;
+}
+
+vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, const int64_t* targets,
+                           const float* lse, const float* entropy, const float* g_logp, const float* g_entropy,
+                           float logit_scale, void* dH_out, void* dW, int32_t dW_dtype, void* ws, size_t ws_bytes,
+                           int32_t* dev_status, void* stream) {
+  vce_status s = check_problem(p);
+  if (s != VCE_OK) return s;
+  if (!(logit_scale > 0.0f) || !std::isfinite(logit_scale)) return VCE_ERR_ARG;
+  if (dW_dtype != VCE_F32 && dW_dtype != VCE_BF16) return VCE_ERR_UNSUPPORTED;
+  // a bf16 dW is the rounded sum of this call alone, and the fp32 problem's dW stays fp32
+  if (dW_dtype == VCE_BF16 && (p->tied_weights || p->dtype != VCE_BF16)) return VCE_ERR_UNSUPPORTED;
+  if (!dW) return VCE_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const size_t row_bytes = static_cast<size_t>(p->H) * (dW_dtype == VCE_BF16 ? 2 : 4);
+  if (p->T == 0) {
+    if (!p->tied_weights) return cuda_status(cudaMemsetAsync(dW, 0, row_bytes * p->Vp, st));
+    return VCE_OK;
+  }
+  if (!h || !W || !lse || !dH_out || (!g_logp && !g_entropy)) return VCE_ERR_ARG;
+  if ((g_logp && !targets) || (g_entropy && !entropy)) return VCE_ERR_ARG;
+  if (!aligned(h, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(lse, 4) || !aligned(entropy, 4) ||
+      !aligned(g_logp, 4) || !aligned(g_entropy, 4) || !aligned(dH_out, 16) || !aligned(dW, 16))
+    return VCE_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, kWsAlign)) return VCE_ERR_WORKSPACE;
+  // Layout: fp32 sum of a bf16 dH | masked h | header | dH K-part counters | G chunk.
+  const size_t acc_bytes = dh_acc_bytes(*p), front = acc_bytes + masked_h_bytes(*p);
+  if (ws_bytes < front) return VCE_ERR_WORKSPACE;
+  float* dH = acc_bytes ? static_cast<float*>(ws) : static_cast<float*>(dH_out);
+  void* hm = static_cast<char*>(ws) + acc_bytes;
+  char* b = static_cast<char*>(ws) + front;
+  ws_bytes -= front;
+  const size_t part_bytes = dh_flag_bytes(*p);
+  const bool use_parts = part_bytes > 0 && ws_bytes >= bwd_bytes_for(*p, 256) + part_bytes;
+  int64_t vc = bwd_chunk_cols(*p, use_parts ? ws_bytes - part_bytes : ws_bytes);
+  if (vc < 256) return VCE_ERR_WORKSPACE;
+  if (vc > (int64_t(1) << 21)) vc = int64_t(1) << 21;   // the fp32 kernels' grids count 64-column blocks in 16 bits
+  int32_t* status = dev_status;
+  if (!status) {
+    status = reinterpret_cast<int32_t*>(b);
+    if (cudaError_t me = cudaMemsetAsync(status, 0, sizeof(int32_t), st)) return cuda_status(me);
+  }
+  int32_t* dh_flags = use_parts ? reinterpret_cast<int32_t*>(b + kBwdHeader) : nullptr;
+  void* G = b + kBwdHeader + (use_parts ? part_bytes : 0);
+  const ProbDev pd = prob_dev(*p);
+  const ScoreGrad sg{lse, entropy, g_logp, g_entropy, logit_scale};
+  const void* hd = h;
+  if (targets) {
+    if (cudaError_t e = launch_mask_rows(h, targets, p->T, pd.V_real, p->ignore_index, p->H * esize_of(*p), hm,
+                                         status, st))
+      return cuda_status(e);
+    hd = hm;
+  }
+  if (!p->tied_weights && p->Vp > p->V_real) {
+    if (cudaError_t me = cudaMemsetAsync(static_cast<char*>(dW) + row_bytes * p->V_real, 0,
+                                         row_bytes * (p->Vp - p->V_real), st))
+      return cuda_status(me);
+  }
+  const bool acc_out = (p->flags & VCE_FLAG_ACCUMULATE_DH) != 0;
+  const bool acc_dh = acc_out && acc_bytes == 0;   // a bf16 dH is added in the rounding step
+  for (int64_t c0 = 0; c0 < p->V_real; c0 += vc) {
+    const int vc_act = static_cast<int>((p->V_real - c0) < vc ? (p->V_real - c0) : vc);
+    cudaError_t e;
+    if (p->dtype == VCE_BF16) {
+      const int parts = dh_flags ? tc_dh_parts(*p, vc_act) : 1;
+      e = launch_tc_bwd_chunk(*p, hd, W, targets, lse, 0.0f, static_cast<int>(c0), vc_act, G, static_cast<int>(vc), dH,
+                              c0 > 0 || acc_dh, dW, p->tied_weights != 0, dh_flags, parts, status, st, &sg,
+                              dW_dtype == VCE_BF16);
+    } else {
+      float* Gf = static_cast<float*>(G);
+      const float* hf = static_cast<const float*>(hd);
+      const float* Wf = static_cast<const float*>(W);
+      e = launch_simt_score_grad(pd, hf, Wf, targets, sg, static_cast<int>(c0), vc_act, Gf, st);
+      if (e == cudaSuccess)   // dH (+)= G W[c0:c0+vc_act]
+        e = launch_sgemm(pd.T, pd.H, vc_act, Gf, vc_act, 1, Wf + c0 * p->H, p->H, 1, dH, p->H,
+                         (c0 > 0 || acc_dh) ? 1 : 0, st);
+      if (e == cudaSuccess)   // dW[c0:c0+vc_act] (+)= G^T h
+        e = launch_sgemm(vc_act, pd.H, pd.T, Gf, 1, vc_act, hf, p->H, 1, static_cast<float*>(dW) + c0 * p->H, p->H,
+                         p->tied_weights ? 1 : 0, st);
+    }
+    if (e != cudaSuccess) return cuda_status(e);
+  }
+  if (acc_bytes) return cuda_status(launch_dh_to_bf16(dH, dH_out, p->T * p->H, acc_out, st));
+  return VCE_OK;
+}
+
+vce_status vce_norm_fwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* bias,
+                        float eps, void* y, float* mean, float* rstd, void* stream) {
+  vce_status s = check_problem(p);
+  if (s != VCE_OK) return s;
+  if (kind != VCE_NORM_LAYER && kind != VCE_NORM_RMS) return VCE_ERR_ARG;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return VCE_ERR_ARG;
+  if (p->T == 0) return VCE_OK;
+  if (!x || !y) return VCE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(mean, 4) ||
+      !aligned(rstd, 4))
+    return VCE_ERR_UNSUPPORTED;
+  return cuda_status(launch_norm_fwd(*p, kind == VCE_NORM_RMS, x, weight, bias, eps, y, mean, rstd,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+vce_status vce_norm_bwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* dy,
+                        const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
+                        int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  vce_status s = check_problem(p);
+  if (s != VCE_OK) return s;
+  if (kind != VCE_NORM_LAYER && kind != VCE_NORM_RMS) return VCE_ERR_ARG;
+  if (accumulate != 0 && accumulate != 1) return VCE_ERR_ARG;
+  if (!dx && !dweight && !dbias) return VCE_ERR_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p->T == 0) {   // the gradient of nothing is zero
+    for (float* g : {dweight, dbias})
+      if (g && !accumulate)
+        if (cudaError_t me = cudaMemsetAsync(g, 0, sizeof(float) * p->H, st)) return cuda_status(me);
+    return VCE_OK;
+  }
+  if (!x || !dy || !rstd || (kind == VCE_NORM_LAYER && !mean)) return VCE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(weight, 16) || !aligned(dy, 16) || !aligned(dx, 16) || !aligned(mean, 4) ||
+      !aligned(rstd, 4) || !aligned(dweight, 16) || !aligned(dbias, 16))
+    return VCE_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, kWsAlign) || ws_bytes < norm_ws_bytes(*p)) return VCE_ERR_WORKSPACE;
+  return cuda_status(launch_norm_bwd(*p, kind == VCE_NORM_RMS, x, weight, dy, (p->flags & VCE_FLAG_DH_BF16) != 0, mean,
+                                     rstd, dx, dweight, dbias, accumulate != 0, ws, st));
 }
 
 vce_status vce_ngram_hash(const int64_t* ids, int64_t T, int32_t n, int64_t V, int64_t M, int64_t seq_len,
