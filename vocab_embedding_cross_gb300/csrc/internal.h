@@ -238,6 +238,12 @@ constexpr int kMaxTop = 32;
 cudaError_t launch_score_rows(const float* Z, int64_t ldz, int64_t rows, int V, int64_t t0, const int64_t* targets,
                               int64_t ignore_index, float scale, int K, float* logp, float* entropy, float* lse,
                               int64_t* top_ids, float* top_logp, int32_t* status, cudaStream_t st);
+// The same from h and W for at most kDecodeTokens tokens (bf16; score_decode.cu).
+constexpr int64_t kDecodeTokens = 128;
+size_t score_decode_ws_bytes(const vce_problem& p, int K);
+cudaError_t launch_score_decode(const vce_problem& p, const void* h, const void* W, const int64_t* targets,
+                                float scale, int K, float* logp, float* entropy, float* lse, int64_t* top_ids,
+                                float* top_logp, void* ws, int32_t* status, cudaStream_t st);
 // out = h with the rows of tokens without a real target set to zero.
 cudaError_t launch_mask_rows(const void* h, const int64_t* targets, int64_t T, int V, int64_t ignore_index,
                              int64_t row_bytes, void* out, int32_t* status, cudaStream_t st);

@@ -209,7 +209,9 @@ int64_t score_rows_per_pass(const vce_problem& p) {
   if (r < 1) r = 1;
   return r < p.T ? r : p.T;
 }
-size_t score_ws_bytes(const vce_problem& p) {
+bool score_decodes(const vce_problem& p) { return p.dtype == VCE_BF16 && p.T <= kDecodeTokens; }
+size_t score_ws_bytes(const vce_problem& p, int K) {
+  if (score_decodes(p)) return score_decode_ws_bytes(p, K);
   return kWsAlign + align_up(static_cast<size_t>(score_rows_per_pass(p)) * static_cast<size_t>(p.Vp) * 4, kWsAlign);
 }
 // The backward's copy of h without the rows of ignored tokens.
@@ -620,7 +622,7 @@ vce_status vce_greedy_argmax(const vce_problem* p, const void* h, const void* W,
 
 size_t vce_logprob_workspace_size(const vce_problem* p, int32_t n_top) {
   if (check_problem(p) != VCE_OK || n_top < 0 || n_top > kMaxTop || n_top > p->V_real) return SIZE_MAX;
-  return score_ws_bytes(*p);
+  return score_ws_bytes(*p, n_top);
 }
 
 vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, const int64_t* targets,
@@ -636,7 +638,7 @@ vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, c
   if (!aligned(h, 16) || !aligned(W, 16) || !aligned(targets, 8) || !aligned(logp, 4) || !aligned(entropy, 4) ||
       !aligned(lse, 4) || !aligned(top_ids, 8) || !aligned(top_logp, 4))
     return VCE_ERR_UNSUPPORTED;
-  if (!ws || !aligned(ws, kWsAlign) || ws_bytes < score_ws_bytes(*p)) return VCE_ERR_WORKSPACE;
+  if (!ws || !aligned(ws, kWsAlign) || ws_bytes < score_ws_bytes(*p, n_top)) return VCE_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* b = static_cast<char*>(ws);
   int32_t* status = dev_status;
@@ -644,6 +646,9 @@ vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, c
     status = reinterpret_cast<int32_t*>(b);
     if (cudaError_t me = cudaMemsetAsync(status, 0, sizeof(int32_t), st)) return cuda_status(me);
   }
+  if (score_decodes(*p))
+    return cuda_status(launch_score_decode(*p, h, W, targets, logit_scale, n_top, logp, entropy, lse, top_ids, top_logp,
+                                           ws, status, st));
   float* Z = reinterpret_cast<float*>(b + kWsAlign);
   const int64_t rows = score_rows_per_pass(*p);
   for (int64_t t0 = 0; t0 < p->T; t0 += rows) {
