@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const uint4* __restrict_
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t y = targets[i / row16];
     const bool valid = y >= 0 && y < V;
-    if (!valid && y != ignore_index) atomicCAS(status, 0, static_cast<int>(VCE_ERR_BAD_INDEX));
+    if (!valid && y != ignore_index && status) atomicCAS(status, 0, static_cast<int>(VCE_ERR_BAD_INDEX));
     out[i] = valid ? h[i] : make_uint4(0, 0, 0, 0);
   }
 }

@@ -6,9 +6,11 @@
 // tile then costs N/128 of a full-width one in tensor time, and no row of W is
 // multiplied by padding tokens. Every CTA owns a contiguous range of classes,
 // equal to within 16 rows whatever V is (a range's last tile is fetched in
-// 16-row boxes), and streams it through a ring of 16 KB tiles: about 190 KB in
-// flight on each SM, several times what hiding the memory latency at full
-// bandwidth takes.
+// 16-row boxes), and streams it through a ring of 32 KB slots, 128 classes by
+// 128 columns of H: 160 to 190 KB in flight on each SM, more than hiding the
+// memory latency at full bandwidth takes. The tokens' columns, which come from
+// L2 again for every tile, have a ring of their own, and each of its slots
+// serves two slots of W.
 //
 // Epilogue (TMEM lane = class, column = token): the logits go to the workspace
 // in fp32 where alternatives are asked for (4 T bytes a class beside the 2 H
@@ -16,7 +18,7 @@
 // tokens at a time to their maximum, S and U by butterfly exchanges that leave
 // token j's sums in lane j, where its running statistics are kept. The merge
 // kernel joins the CTAs' statistics and takes the alternatives from the
-// 32-class groups whose maximum can reach the K-th largest one.
+// 16-class groups whose maximum can reach the K-th largest one.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -30,35 +32,44 @@
 namespace vce {
 namespace {
 
-constexpr int kRows = 128;                 // classes per tile (the MMA's M)
-constexpr int kBlockK = 64;
+constexpr int kSub = 128;                  // classes per MMA (its M)
+constexpr int kRows = 256;                 // classes per tile: two MMA row blocks
+constexpr int kPanel = 64;                 // columns of H per 128-byte swizzled panel
+constexpr int kBlockK = 128;               // columns of H per slot: two panels
 constexpr int kBatch = 16;                 // tokens reduced at a time
-constexpr uint32_t kWBytes = kRows * kBlockK * 2;
+constexpr uint32_t kPanelBytes = kSub * kPanel * 2;
+constexpr uint32_t kWBytes = 2 * kPanelBytes;      // one slot of W
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int N>
 struct Dec {
-  static constexpr int epi_warps = N <= 32 ? 4 : N / 8;   // each warp: 32 classes, at most 32 tokens
+  // Each epilogue warp: 32 classes of a row block, at most 32 tokens. Up to 32
+  // tokens the two row blocks of a tile have warps of their own.
+  static constexpr int sub_warps = N <= 32 ? 2 : 1;
+  static constexpr int epi_warps = N <= 32 ? 8 : N / 8;
   static constexpr int threads = 64 + 32 * epi_warps;
   static constexpr int tokens = N <= 32 ? N : 32;         // per epilogue warp
-  static constexpr uint32_t stage_bytes = kWBytes + N * kBlockK * 2;
-  static constexpr int stages = static_cast<int>((208 * 1024) / stage_bytes);
-  static constexpr uint32_t tmem_cols = 2 * N < 32 ? 32 : 2 * N;
-  static constexpr size_t smem = 1024 + static_cast<size_t>(stages) * stage_bytes + 512;
-  static constexpr uint32_t idesc = idesc_bf16_f32(kRows, N, 0, 0);
+  static constexpr int parts = 4 * sub_warps;             // partial statistics of a token per CTA
+  static constexpr uint32_t h_bytes = N * kBlockK * 2;    // one slot of the tokens' ring
+  static constexpr int w_slots = N <= 32 ? 6 : 5;
+  static constexpr int h_slots = static_cast<int>((224 * 1024 - w_slots * kWBytes) / h_bytes) < w_slots
+                                     ? static_cast<int>((224 * 1024 - w_slots * kWBytes) / h_bytes)
+                                     : w_slots;
+  static constexpr uint32_t tmem_cols = 4 * N;            // two tiles of two row blocks
+  static constexpr size_t smem = 1024 + static_cast<size_t>(w_slots) * kWBytes + h_slots * h_bytes + 512;
+  static constexpr uint32_t idesc = idesc_bf16_f32(kSub, N, 0, 0);
 };
 
 struct DecArgs {
-  int T, V, num_kb;
-  int groups;          // 16-class groups of the vocabulary
+  int T, V, H, num_kb;
+  int groups, ldg;     // 16-class groups of the vocabulary, and the row stride of gmax
   float scale;
   const int64_t* targets;
   float* Z;            // [T, ldz] logits, or null
   int64_t ldz;
-  uint32_t* gmax;      // [T, n_cta * gpc] ordered maxima of 32-class groups, or null
-  int gpc;
-  float4* part;        // [T, n_cta * 4] (m, S, U)
+  uint32_t* gmax;      // [T, ldg] ordered maxima of the 16-class groups, or null
+  float4* part;        // [T, n_cta * parts] (m, S, U)
   float* ztgt;         // [T] target logits, written by the class's owner
   int32_t* status;
   uint64_t limit_ns;
@@ -68,7 +79,8 @@ __host__ __device__ __forceinline__ int dec_row0(int groups, int n_cta, int cta)
   return static_cast<int>(static_cast<int64_t>(groups) * cta / n_cta) * 16;
 }
 
-// Sums (or maxima) of v[0..15] over the warp: lane l ends with that of v[l & 15].
+// Sums (or maxima) of v[0..15] over the lane's half of the warp: lane l ends
+// with that of v[l & 15].
 template <bool MAX>
 __device__ __forceinline__ float butterfly16(float (&v)[kBatch], int lane) {
 #pragma unroll
@@ -81,9 +93,9 @@ __device__ __forceinline__ float butterfly16(float (&v)[kBatch], int lane) {
       v[i] = MAX ? fmaxf(keep, got) : keep + got;
     }
   }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 16);
-  return MAX ? fmaxf(v[0], got) : v[0] + got;
+  return v[0];
 }
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor_sync(0xffffffffu, v, 16); }
 
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -95,19 +107,91 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
+// Position in a ring of slots; `phase` is the parity of the slot's current use.
+template <int SLOTS>
+struct Ring {
+  int slot = 0;
+  uint32_t phase = 0;
+  bool wrapped = false;
+  __device__ __forceinline__ void next() {
+    if (++slot == SLOTS) {
+      slot = 0;
+      phase ^= 1u;
+      wrapped = true;
+    }
+  }
+  // Waits (at most 100 ms in all) for the last use of every slot filled so far.
+  __device__ __forceinline__ void drain(uint64_t* full, uint64_t t0) const {
+    for (int s = 0; s < (wrapped ? SLOTS : slot); ++s)
+      while (!mbar_try_wait(&full[s], s < slot ? phase : phase ^ 1u) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+  }
+};
+
+// A try that the hardware may suspend for up to 20 us before it says no.
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait for a pipeline that often has to wait: the clock is read only after
+// 64 unsuccessful tries, each of which the hardware suspends for a while.
+__device__ __noinline__ bool wait_later(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (try_wait_long(bar, parity)) return true;
+    if ((it & 63u) == 0u) {
+      if (*w.abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > w.limit_ns) {
+        *w.abort = 1;
+        record_status(w.status, 5);
+        return false;
+      }
+    }
+  }
+}
+// A whole warp's wait; the answer is the same in every lane.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || __all_sync(0xffffffffu, wait_later(bar, parity, w));
+}
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool wait_late(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return mbar_try_wait(bar, parity) || wait_later(bar, parity, w);
+}
+
 template <int N>
 __global__ void __launch_bounds__(Dec<N>::threads, 1)
     score_decode_kernel(const __grid_constant__ CUtensorMap mapW, const __grid_constant__ CUtensorMap mapW16,
                         const __grid_constant__ CUtensorMap mapH, const DecArgs a) {
   using D = Dec<N>;
-  constexpr int kStages = D::stages;
+  constexpr int kW = D::w_slots, kH = D::h_slots;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* tail = smem_raw + (base - raw) + kStages * D::stage_bytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(tail);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
+  const uint32_t base = (raw + 1023u) & ~1023u, base_h = base + kW * kWBytes;
+  uint8_t* tail = smem_raw + (base - raw) + kW * kWBytes + kH * D::h_bytes;
+  uint64_t* wfull = reinterpret_cast<uint64_t*>(tail);
+  uint64_t* wempty = wfull + kW;
+  uint64_t* hfull = wempty + kW;
+  uint64_t* hempty = hfull + kH;
+  uint64_t* tfull = hempty + kH;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
@@ -116,9 +200,13 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
   const int cta = blockIdx.x, n_cta = gridDim.x;
   grid_dep_launch();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    for (int s = 0; s < kW; ++s) {
+      mbar_init(&wfull[s], 1);
+      mbar_init(&wempty[s], 1);
+    }
+    for (int s = 0; s < kH; ++s) {
+      mbar_init(&hfull[s], 1);
+      mbar_init(&hempty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
@@ -141,97 +229,102 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
   const int n_tiles = (row_hi - row_lo + kRows - 1) / kRows;
   grid_dep_wait();
 
+  // The two feeding warps run their loops whole and elect one lane for each
+  // issue, so that ring positions and descriptors stay in uniform registers:
+  // with a single active lane the issue of four small MMAs took 385 cycles,
+  // longer than their 16 KB of W take to arrive.
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       tma_prefetch_desc(&mapW);
       tma_prefetch_desc(&mapW16);
       tma_prefetch_desc(&mapH);
-      int stage = 0;
-      uint32_t phase = 0;
-      int last_parity[kStages];
-#pragma unroll
-      for (int s = 0; s < kStages; ++s) last_parity[s] = -1;
-      bool ok = true, issued = false;
-      for (int tt = 0; ok && tt < n_tiles; ++tt) {
-        const int r0 = row_lo + tt * kRows;
-        const int rows = row_hi - r0 < kRows ? row_hi - r0 : kRows;   // a multiple of 16
-        for (int kb = 0; kb < a.num_kb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sW = base + static_cast<uint32_t>(stage) * D::stage_bytes;
-          mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(rows) * 128u + N * 128u);
-          if (rows == kRows)
-            tma_load_2d(sW, &mapW, &full[stage], kb * kBlockK, r0);
-          else
-            for (int r = 0; r < rows; r += 16)
-              tma_load_2d(sW + static_cast<uint32_t>(r) * 128u, &mapW16, &full[stage], kb * kBlockK, r0 + r);
-          tma_load_2d(sW + kWBytes, &mapH, &full[stage], kb * kBlockK, 0);
-          issued = true;
-          last_parity[stage] = static_cast<int>(phase);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+    }
+    Ring<kW> w;
+    Ring<kH> hr;
+    bool ok = true;
+    for (int tt = 0; ok && tt < n_tiles; ++tt) {
+      const int r0 = row_lo + tt * kRows;
+      const int rows = row_hi - r0 < kRows ? row_hi - r0 : kRows;   // a multiple of 16
+      for (int kb = 0; ok && kb < a.num_kb; ++kb) {
+        if (!(ok = wait_warp(&hempty[hr.slot], hr.phase ^ 1u, wc))) break;
+        const int k0 = kb * kBlockK, panels = a.H - k0 > kPanel ? 2 : 1;
+        if (elect_one()) {
+          const uint32_t sH = base_h + static_cast<uint32_t>(hr.slot) * D::h_bytes;
+          mbar_arrive_expect_tx(&hfull[hr.slot], static_cast<uint32_t>(panels) * (N * 128u));
+          for (int j = 0; j < panels; ++j) tma_load_2d(sH + j * (N * 128u), &mapH, &hfull[hr.slot], k0 + j * kPanel, 0);
         }
-      }
-      if (!ok && issued) {   // let the copies already issued land
-        const uint64_t t0 = globaltimer_ns();
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-          if (last_parity[s] < 0) continue;
-          while (!mbar_try_wait(&full[s], static_cast<uint32_t>(last_parity[s])) &&
-                 globaltimer_ns() - t0 < 100000000ull) {
+        hr.next();
+        for (int s0 = 0; s0 < rows; s0 += kSub) {
+          if (!(ok = wait_warp(&wempty[w.slot], w.phase ^ 1u, wc))) break;
+          const int n = rows - s0 < kSub ? rows - s0 : kSub;
+          const uint32_t sW = base + static_cast<uint32_t>(w.slot) * kWBytes;
+          if (elect_one()) {
+            mbar_arrive_expect_tx(&wfull[w.slot], static_cast<uint32_t>(panels * n) * 128u);
+            for (int j = 0; j < panels; ++j) {
+              const uint32_t sP = sW + static_cast<uint32_t>(j) * kPanelBytes;
+              if (n == kSub)
+                tma_load_2d(sP, &mapW, &wfull[w.slot], k0 + j * kPanel, r0 + s0);
+              else
+                for (int r = 0; r < n; r += 16)
+                  tma_load_2d(sP + static_cast<uint32_t>(r) * 128u, &mapW16, &wfull[w.slot], k0 + j * kPanel, r0 + s0 + r);
+            }
           }
+          w.next();
         }
       }
     }
+    if (!ok && lane == 0) {   // let the copies already issued land
+      const uint64_t t0 = globaltimer_ns();
+      w.drain(wfull, t0);
+      hr.drain(hfull, t0);
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true, issued = false;
-      for (int tt = 0; ok && tt < n_tiles; ++tt) {
-        const int acc = tt & 1;
-        if (!mbar_wait(&tempty[acc], ((tt >> 1) & 1) ^ 1, wc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * N);
-        for (int kb = 0; kb < a.num_kb; ++kb) {
-          if (!mbar_wait(&full[stage], phase, wc)) {
-            ok = false;
-            break;
-          }
+    Ring<kW> w;
+    Ring<kH> hr;
+    bool ok = true, issued = false;
+    for (int tt = 0; ok && tt < n_tiles; ++tt) {
+      const int acc = tt & 1;
+      if (!(ok = wait_warp(&tempty[acc], ((tt >> 1) & 1) ^ 1, wc))) break;
+      tc_fence_after();
+      const uint32_t d = tmem + static_cast<uint32_t>(acc * 2 * N);
+      const int subs = row_hi - (row_lo + tt * kRows) > kSub ? 2 : 1;   // row blocks that hold a class
+      for (int kb = 0; ok && kb < a.num_kb; ++kb) {
+        if (!(ok = wait_warp(&hfull[hr.slot], hr.phase, wc))) break;
+        const int panels = a.H - kb * kBlockK > kPanel ? 2 : 1;
+        const uint64_t bd = smem_desc_sw128(base_h + static_cast<uint32_t>(hr.slot) * D::h_bytes, 16u, 1024u);
+        for (int s0 = 0; s0 < subs; ++s0) {
+          if (!(ok = wait_warp(&wfull[w.slot], w.phase, wc))) break;
           tc_fence_after();
-          const uint32_t sW = base + static_cast<uint32_t>(stage) * D::stage_bytes;
-          const uint64_t ad = smem_desc_sw128(sW, 16u, 1024u), bd = smem_desc_sw128(sW + kWBytes, 16u, 1024u);
+          const uint64_t ad = smem_desc_sw128(base + static_cast<uint32_t>(w.slot) * kWBytes, 16u, 1024u);
+          if (elect_one()) {
+            for (int j = 0; j < panels; ++j)
 #pragma unroll
-          for (int kk = 0; kk < kBlockK / 16; ++kk)
-            umma_f16(d, ad + static_cast<uint64_t>(kk * 2), bd + static_cast<uint64_t>(kk * 2), D::idesc,
-                     (kb != 0 || kk != 0) ? 1u : 0u);
-          issued = true;
-          umma_commit(&empty[stage]);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
+              for (int kk = 0; kk < kPanel / 16; ++kk)
+                umma_f16(d + static_cast<uint32_t>(s0 * N), ad + static_cast<uint64_t>(j * (kPanelBytes >> 4) + kk * 2),
+                         bd + static_cast<uint64_t>(j * (N * 128u >> 4) + kk * 2), D::idesc,
+                         (kb != 0 || j != 0 || kk != 0) ? 1u : 0u);
+            umma_commit(&wempty[w.slot]);
+            if (s0 == subs - 1) umma_commit(&hempty[hr.slot]);
+            if (s0 == subs - 1 && kb == a.num_kb - 1) umma_commit(&tfull[acc]);
           }
+          __syncwarp();
+          issued = true;
+          w.next();
         }
-        if (ok) umma_commit(&tfull[acc]);
+        hr.next();
       }
-      if (!ok && issued) {   // wait for the MMAs in flight before TMEM is released
-        umma_commit(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < 100000000ull) {
-        }
+    }
+    if (!ok && issued && elect_one()) {   // wait for the MMAs in flight before TMEM is released
+      umma_commit(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < 100000000ull) {
       }
     }
   } else {
     const int e = warp - 2;
     const int q = warp & 3;                  // TMEM lane quarter this warp may read
-    const int tok0 = (e >> 2) * D::tokens;   // its first token
+    const int sub0 = D::sub_warps == 2 ? e >> 2 : 0;
+    const int tok0 = D::sub_warps == 2 ? 0 : (e >> 2) * D::tokens;   // its first token
     constexpr int kB = D::tokens / kBatch;
     float m_run[kB], s_run[kB], u_run[kB];   // of token tok0 + 16 b + (lane & 15)
     int64_t y[kB];
@@ -245,65 +338,73 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
     const float sL = a.scale * kLog2e;
     for (int tt = 0; tt < n_tiles; ++tt) {
       const int acc = tt & 1;
-      if (!mbar_wait(&tfull[acc], (tt >> 1) & 1, wc)) break;
+      // one lane waits: eight polling warps would take issue slots from the two
+      // threads that feed the pipeline
+      const bool go = lane == 0 ? wait_late(&tfull[acc], (tt >> 1) & 1, wc) : true;
+      if (!__shfl_sync(0xffffffffu, go, 0)) break;
       tc_fence_after();
-      const int r0 = row_lo + tt * kRows + q * 32;      // first class of this warp's 32
-      const int v = r0 + lane;
-      const bool row_ok = v < row_hi && v < a.V;
+#pragma unroll 1
+      for (int sub = sub0; sub < sub0 + 3 - D::sub_warps; ++sub) {
+        const int r0 = row_lo + tt * kRows + sub * kSub + q * 32;      // first class of this warp's 32
+        const int v = r0 + lane;
+        const bool row_ok = v < row_hi && v < a.V;
 #pragma unroll
-      for (int b = 0; b < kB; ++b) {
-        const int t0 = tok0 + b * kBatch;
-        uint32_t x[kBatch];
-        tmem_ld_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * N + t0), x);
-        tmem_ld_wait();
+        for (int b = 0; b < kB; ++b) {
+          const int t0 = tok0 + b * kBatch;
+          uint32_t x[kBatch];
+          tmem_ld_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>((acc * 2 + sub) * N + t0), x);
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) asm volatile("" : "+r"(x[j]));
-        if (b == kB - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[acc]);
-        }
-        if (t0 >= a.T || r0 >= row_hi) continue;        // the same for the whole warp
-        float mx[kBatch];
+          for (int j = 0; j < kBatch; ++j) asm volatile("" : "+r"(x[j]));
+          if (b == kB - 1 && sub == sub0 + 2 - D::sub_warps) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[acc]);
+          }
+          if (t0 >= a.T || r0 >= row_hi) continue;        // the same for the whole warp
+          float mx[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) mx[j] = row_ok ? __uint_as_float(x[j]) : -INFINITY;
-        if (a.Z && row_ok) {
+          for (int j = 0; j < kBatch; ++j) mx[j] = row_ok ? __uint_as_float(x[j]) : -INFINITY;
+          if (a.Z && row_ok) {
 #pragma unroll
-          for (int j = 0; j < kBatch; ++j)
-            if (t0 + j < a.T) a.Z[static_cast<int64_t>(t0 + j) * a.ldz + v] = __uint_as_float(x[j]);
-        }
-        const float gm = butterfly16<true>(mx, lane);   // of token t0 + (lane & 15)
-        const int64_t off = y[b] - r0;                  // the target, if it is one of the warp's classes
-        if (__any_sync(0xffffffffu, off >= 0 && off < 32)) {
+            for (int j = 0; j < kBatch; ++j)
+              if (t0 + j < a.T) a.Z[static_cast<int64_t>(t0 + j) * a.ldz + v] = __uint_as_float(x[j]);
+          }
+          // token t0 + (lane & 15): maximum of the lane's 16 classes, then of the warp's 32
+          const float hm = butterfly16<true>(mx, lane);
+          const float gm = fmaxf(hm, other_half(hm));
+          if (a.gmax && t0 + (lane & 15) < a.T && r0 + (lane & 16) < row_hi)
+            a.gmax[static_cast<int64_t>(t0 + (lane & 15)) * a.ldg + ((r0 + lane) >> 4)] = hm == hm ? ordered_bits(hm) : 0u;
+          const int64_t off = y[b] - r0;                  // the target, if it is one of the warp's classes
+          if (__any_sync(0xffffffffu, off >= 0 && off < 32)) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+              const int at = static_cast<int>(__shfl_sync(0xffffffffu, off >= 0 && off < 32 ? static_cast<int>(off) : -1, j));
+              if (at == lane && row_ok) a.ztgt[t0 + j] = __uint_as_float(x[j]);
+            }
+          }
+          const float ref = gm == -INFINITY ? 0.0f : gm;  // no finite logit: exp(-inf) = 0 against any reference
+          float ex[kBatch], ux[kBatch];
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) {
-            const int at = static_cast<int>(__shfl_sync(0xffffffffu, off >= 0 && off < 32 ? static_cast<int>(off) : -1, j));
-            if (at == lane && row_ok) a.ztgt[t0 + j] = __uint_as_float(x[j]);
+            const float d = (__uint_as_float(x[j]) - __shfl_sync(0xffffffffu, ref, j)) * sL;
+            ex[j] = row_ok ? ex2_approx(d) : 0.0f;
+            ux[j] = row_ok ? ex[j] * fmaxf(d, -300.0f) : 0.0f;   // 2^-300 is 0: keeps 0 * -inf out
           }
+          const float Sh = butterfly16<false>(ex, lane), Uh = butterfly16<false>(ux, lane);
+          const float S = Sh + other_half(Sh), U = (Uh + other_half(Uh)) * kLn2;
+          const ScoreStat r = score_stat_join(ScoreStat{m_run[b], s_run[b], u_run[b]}, ScoreStat{gm * a.scale, S, U});
+          m_run[b] = r.m;
+          s_run[b] = r.S;
+          u_run[b] = r.U;
         }
-        const float ref = gm == -INFINITY ? 0.0f : gm;  // no finite logit: exp(-inf) = 0 against any reference
-        float ex[kBatch], ux[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const float d = (__uint_as_float(x[j]) - __shfl_sync(0xffffffffu, ref, j)) * sL;
-          ex[j] = row_ok ? ex2_approx(d) : 0.0f;
-          ux[j] = row_ok ? ex[j] * fmaxf(d, -300.0f) : 0.0f;   // 2^-300 is 0: keeps 0 * -inf out
-        }
-        const float S = butterfly16<false>(ex, lane), U = butterfly16<false>(ux, lane) * kLn2;
-        const ScoreStat r = score_stat_join(ScoreStat{m_run[b], s_run[b], u_run[b]}, ScoreStat{gm * a.scale, S, U});
-        m_run[b] = r.m;
-        s_run[b] = r.S;
-        u_run[b] = r.U;
-        if (a.gmax && lane < kBatch && t0 + lane < a.T)
-          a.gmax[static_cast<int64_t>(t0 + lane) * n_cta * a.gpc + static_cast<int64_t>(cta) * a.gpc + tt * 4 + q] =
-              gm == gm ? ordered_bits(gm) : 0u;
       }
     }
 #pragma unroll
     for (int b = 0; b < kB; ++b) {
       const int t = tok0 + b * kBatch + lane;
       if (lane < kBatch && t < a.T)
-        a.part[(static_cast<int64_t>(t) * n_cta + cta) * 4 + q] = make_float4(m_run[b], s_run[b], u_run[b], 0.0f);
+        a.part[(static_cast<int64_t>(t) * n_cta + cta) * D::parts + sub0 * 4 + q] = make_float4(m_run[b], s_run[b], u_run[b], 0.0f);
     }
   }
   __syncwarp();
@@ -315,47 +416,79 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
   }
 }
 
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 1024;
 constexpr int kMergeCand = 1024;
+constexpr int kMergeLists = 64;    // group lists whose maxima give the bound (at least kMaxTop)
+constexpr int kMergePick = 512;    // groups read for candidates
+constexpr int kMergeKeep = 3;      // quadruples of group maxima that each thread keeps in registers
 
-// One block per token. A group of 32 classes with maximum g holds a key of at
-// least (g, its last class), so the K-th largest such key over the threads'
-// best groups bounds the K-th largest key of the row from below; only groups
-// that reach (g, first class) >= the bound are read. Equal logits do not widen
-// the choice: an all-equal row reads the first K groups.
+// One block per token. A group of 16 classes with maximum g holds a key of at
+// least (g, its last class), so the K-th largest such key over 64 disjoint
+// lists' best groups bounds the K-th largest key of the row from below; only
+// groups that reach (g, first class) >= the bound are read, one half-warp each.
+// Equal logits do not widen the choice: an all-equal row reads about the first
+// K groups.
 __global__ void __launch_bounds__(kMergeThreads)
-    score_merge_kernel(int V, int groups, int n_cta, int gpc, const float4* __restrict__ part,
+    score_merge_kernel(int V, int groups, int ldg, int n_part, const float4* __restrict__ part,
                        const uint32_t* __restrict__ gmax, const float* __restrict__ Z, int64_t ldz,
                        const float* __restrict__ ztgt, const int64_t* __restrict__ targets, int64_t ignore_index,
                        float scale, int K, float* __restrict__ logp, float* __restrict__ entropy,
                        float* __restrict__ lse, int64_t* __restrict__ top_ids, float* __restrict__ top_logp,
                        int32_t* status) {
-  __shared__ ScoreStat sstat[kMergeThreads / 32];
-  __shared__ uint64_t skey[kMergeThreads];
+  constexpr int kWarps = kMergeThreads / 32;
+  static_assert(kWarps == 32, "one partial per lane");
+  __shared__ ScoreStat sstat[kWarps];
+  __shared__ uint64_t skey[kMergeLists];
   __shared__ uint64_t cand[kMergeCand];
   __shared__ uint64_t best[kMaxTop];
+  __shared__ int pick[kMergePick];
   __shared__ uint64_t s_bound;
-  __shared__ int s_n;
+  __shared__ int s_n, s_pick;
   grid_dep_launch();
-  grid_dep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t t = blockIdx.x;
+  if (tid < kMaxTop) best[tid] = 0;
+  if (tid < kMergeLists) skey[tid] = 0;
+  if (tid == 0) {
+    s_n = s_pick = 0;
+    s_bound = 0;
+  }
+  __syncthreads();
+  grid_dep_wait();
   ScoreStat a = score_stat_empty();
-  for (int i = tid; i < 4 * n_cta; i += kMergeThreads) {
-    const float4 p = part[t * 4 * n_cta + i];
+  for (int i = tid; i < n_part; i += kMergeThreads) {
+    const float4 p = part[t * n_part + i];
     a = score_stat_join(a, ScoreStat{p.x, p.y, p.z});
   }
-  // Group i of CTA c starts at dec_row0(c) + 32 i; slots past the CTA's range are never written.
+  // Thread i reads group quadruples i, i + 1024, ...; the first kMergeKeep stay in registers.
   uint64_t kmax = 0;
-  const uint32_t* gm = K ? gmax + t * n_cta * gpc : nullptr;
-  for (int i = tid; K && i < n_cta * gpc; i += kMergeThreads) {
-    const int c = i / gpc, v0 = dec_row0(groups, n_cta, c) + (i - c * gpc) * 32;
-    const int hi = min(dec_row0(groups, n_cta, c + 1), V);
-    const uint32_t g = v0 < hi ? gm[i] : 0;
-    if (g) {
-      const uint64_t k = (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(min(v0 + 32, hi) - 1));
-      kmax = k > kmax ? k : kmax;
+  const uint4* gm = K ? reinterpret_cast<const uint4*>(gmax + t * ldg) : nullptr;
+  const int quads = (groups + 3) >> 2;
+  auto low_key = [&](uint32_t g, int i) {   // 0 for a group of NaN alone, and past the last group
+    return g && i < groups ? (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(min(16 * i + 16, V) - 1)) : 0;
+  };
+  auto high_key = [&](uint32_t g, int i) {
+    return g && i < groups ? (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(16 * i)) : 0;
+  };
+  uint4 keep[kMergeKeep];
+  if (K) {
+    auto raise = [&](const uint4& g, int quad) {
+      const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t k = low_key(w[j], 4 * quad + j);
+        kmax = k > kmax ? k : kmax;
+      }
+    };
+#pragma unroll
+    for (int c = 0; c < kMergeKeep; ++c) {
+      const int quad = tid + c * kMergeThreads;
+      keep[c] = quad < quads ? gm[quad] : make_uint4(0, 0, 0, 0);
     }
+#pragma unroll
+    for (int c = 0; c < kMergeKeep; ++c) raise(keep[c], tid + c * kMergeThreads);
+    for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) raise(gm[quad], quad);
+    atomicMax(reinterpret_cast<unsigned long long*>(&skey[tid & (kMergeLists - 1)]), static_cast<unsigned long long>(kmax));
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -364,40 +497,55 @@ __global__ void __launch_bounds__(kMergeThreads)
     a = (lane & o) == 0 ? score_stat_join(a, b) : score_stat_join(b, a);
   }
   if (lane == 0) sstat[warp] = a;
-  skey[tid] = kmax;
-  if (tid < K) best[tid] = 0;
-  if (tid == 0) {
-    s_n = 0;
-    s_bound = 0;
-  }
   __syncthreads();
-  a = sstat[0];
-  for (int w = 1; w < kMergeThreads / 32; ++w) a = score_stat_join(a, sstat[w]);
+  if (K && tid < kMergeLists) {
+    const uint64_t k = skey[tid];
+    int rank = 0;
+#pragma unroll 16
+    for (int i = 0; i < kMergeLists; ++i) rank += skey[i] > k ? 1 : 0;
+    if (k && rank == K - 1) s_bound = k;   // stays 0 when fewer than K lists hold a group
+  }
+  // every warp joins the 32 warps' statistics
+  a = sstat[lane];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ScoreStat b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.S, o),
+                __shfl_xor_sync(0xffffffffu, a.U, o)};
+    a = (lane & o) == 0 ? score_stat_join(a, b) : score_stat_join(b, a);
+  }
   const float l = score_lse(a);
-  if (tid == 0) {
+  if (tid == kMergeThreads - 1) {
     if (lse) lse[t] = l;
     const int64_t y = targets ? targets[t] : -1;
     const bool valid = targets && y >= 0 && y < V;
-    if (targets && !valid && y != ignore_index) atomicCAS(status, 0, static_cast<int>(VCE_ERR_BAD_INDEX));
+    if (targets && !valid && y != ignore_index && status) atomicCAS(status, 0, static_cast<int>(VCE_ERR_BAD_INDEX));
     if (logp) logp[t] = valid ? fmaf(ztgt[t], scale, -l) : 0.0f;
     if (entropy) entropy[t] = (!targets || valid) ? score_entropy(a) : 0.0f;
   }
   if (K == 0) return;
-  if (kmax) {
-    int rank = 0;
-    for (int i = 0; i < kMergeThreads; ++i) rank += skey[i] > kmax ? 1 : 0;
-    if (rank == K - 1) s_bound = kmax;   // stays 0 when fewer than K threads hold a group
-  }
   __syncthreads();
   const uint64_t bound = s_bound;
   const float* z = Z + t * ldz;
-  for (int i = tid; i < n_cta * gpc; i += kMergeThreads) {
-    const int c = i / gpc, v0 = dec_row0(groups, n_cta, c) + (i - c * gpc) * 32;
-    const int hi = min(dec_row0(groups, n_cta, c + 1), V);
-    const uint32_t g = v0 < hi ? gm[i] : 0;
-    if (!g || ((static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(v0))) < bound) continue;
-    for (int v = v0; v < min(v0 + 32, hi); ++v) {
-      const uint64_t k = top_key(z[v], static_cast<uint32_t>(v));
+  auto choose = [&](const uint4& g, int quad) {
+    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t k = high_key(w[j], 4 * quad + j);
+      if (k != 0 && k >= bound) {
+        const int at = atomicAdd(&s_pick, 1);
+        if (at < kMergePick) pick[at] = 4 * quad + j;
+      }
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < kMergeKeep; ++c) choose(keep[c], tid + c * kMergeThreads);
+  for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) choose(gm[quad], quad);
+  __syncthreads();
+  const int n_pick = s_pick;
+  if (n_pick <= kMergePick) {
+    for (int i = tid >> 4; i < n_pick; i += kMergeThreads / 16) {
+      const int v = 16 * pick[i] + (lane & 15);
+      const uint64_t k = v < V ? top_key(z[v], static_cast<uint32_t>(v)) : 0;
       if (k != 0 && k >= bound) {
         const int at = atomicAdd(&s_n, 1);
         if (at < kMergeCand) cand[at] = k;
@@ -406,17 +554,18 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
   __syncthreads();
   const int n = s_n;
-  if (n <= kMergeCand) {
+  if (n_pick <= kMergePick && n <= kMergeCand) {
     for (int i = tid; i < n; i += kMergeThreads) {
       const uint64_t k = cand[i];
       int r = 0;
+#pragma unroll 8
       for (int j = 0; j < n; ++j) r += cand[j] > k ? 1 : 0;
       if (r < K) best[r] = k;
     }
     __syncthreads();
   } else {
-    // Over kMergeCand keys reach the bound (the largest logits all in a few
-    // threads' groups): K scans, each for the largest key below the last.
+    // Too many reach the bound (the largest logits all in a few lists): K
+    // scans of the row, each for the largest key below the last.
     uint64_t below = ~uint64_t(0);
     for (int i = 0; i < K; ++i) {
       uint64_t k = 0;
@@ -433,7 +582,7 @@ __global__ void __launch_bounds__(kMergeThreads)
       if (lane == 0) skey[warp] = k;
       __syncthreads();
       below = skey[0];
-      for (int w = 1; w < kMergeThreads / 32; ++w) below = skey[w] > below ? skey[w] : below;
+      for (int w = 1; w < kWarps; ++w) below = skey[w] > below ? skey[w] : below;
       if (tid == 0) best[i] = below;
     }
     __syncthreads();
@@ -442,7 +591,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 struct DecLayout {
-  int n_cta, groups, gpc;
+  int n_cta, groups, ldg, parts;
   size_t part, ztgt, gmax, Z, total;
 };
 DecLayout dec_layout(const vce_problem& p, int K) {
@@ -450,18 +599,18 @@ DecLayout dec_layout(const vce_problem& p, int K) {
   L.groups = static_cast<int>(ceil_div(p.V_real, 16));
   const int sms = current_device_info().num_sms;
   L.n_cta = L.groups < sms ? L.groups : sms;
-  // a range holds at most ceil(groups / n_cta) groups, in tiles of 8 of them
-  L.gpc = static_cast<int>(ceil_div(ceil_div(L.groups, L.n_cta), 8)) * 4;
-  size_t off = kWsAlign;   // status word
+  L.ldg = (L.groups + 3) / 4 * 4;
+  L.parts = p.T <= 32 ? Dec<32>::parts : Dec<128>::parts;
+  size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes, kWsAlign);
     return o;
   };
   const size_t T = static_cast<size_t>(p.T);
-  L.part = take(T * 4 * L.n_cta * sizeof(float4));
+  L.part = take(T * L.parts * L.n_cta * sizeof(float4));
   L.ztgt = take(T * sizeof(float));
-  L.gmax = take(K ? T * L.n_cta * L.gpc * sizeof(uint32_t) : 0);
+  L.gmax = take(K ? T * L.ldg * sizeof(uint32_t) : 0);
   L.Z = take(K ? T * static_cast<size_t>(p.Vp) * sizeof(float) : 0);
   L.total = off;
   return L;
@@ -480,9 +629,9 @@ cudaError_t launch_n(const vce_problem& p, const void* h, const void* W, const D
   }
   CUtensorMap mw, mw16, mh;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!make_tmap_2d(&mw, W, BF, 2, p.H, p.V_real, p.H, kBlockK, kRows, true) ||
-      !make_tmap_2d(&mw16, W, BF, 2, p.H, p.V_real, p.H, kBlockK, 16, true) ||
-      !make_tmap_2d(&mh, h, BF, 2, p.H, p.T, p.H, kBlockK, N, true))
+  if (!make_tmap_2d(&mw, W, BF, 2, p.H, p.V_real, p.H, kPanel, kSub, true) ||
+      !make_tmap_2d(&mw16, W, BF, 2, p.H, p.V_real, p.H, kPanel, 16, true) ||
+      !make_tmap_2d(&mh, h, BF, 2, p.H, p.T, p.H, kPanel, N, true))
     return cudaErrorInvalidValue;
   const cudaError_t e = launch_dependent(score_decode_kernel<N>, dim3(static_cast<unsigned>(L.n_cta)),
                                          dim3(D::threads), D::smem, st, mw, mw16, mh, a);
@@ -502,14 +651,15 @@ cudaError_t launch_score_decode(const vce_problem& p, const void* h, const void*
   DecArgs a{};
   a.T = static_cast<int>(p.T);
   a.V = static_cast<int>(p.V_real);
+  a.H = static_cast<int>(p.H);
   a.num_kb = static_cast<int>(ceil_div(p.H, kBlockK));
   a.groups = L.groups;
+  a.ldg = L.ldg;
   a.scale = scale;
   a.targets = targets;
   a.Z = K ? reinterpret_cast<float*>(b + L.Z) : nullptr;
   a.ldz = p.Vp;
   a.gmax = K ? reinterpret_cast<uint32_t*>(b + L.gmax) : nullptr;
-  a.gpc = L.gpc;
   a.part = reinterpret_cast<float4*>(b + L.part);
   a.ztgt = reinterpret_cast<float*>(b + L.ztgt);
   a.status = status;
@@ -520,7 +670,7 @@ cudaError_t launch_score_decode(const vce_problem& p, const void* h, const void*
                               : launch_n<128>(p, h, W, L, a, st);
   if (e != cudaSuccess) return e;
   e = launch_dependent(score_merge_kernel, dim3(static_cast<unsigned>(p.T)), dim3(kMergeThreads), 0, st, a.V, L.groups,
-                       L.n_cta, L.gpc, static_cast<const float4*>(a.part), static_cast<const uint32_t*>(a.gmax),
+                       L.ldg, L.parts * L.n_cta, static_cast<const float4*>(a.part), static_cast<const uint32_t*>(a.gmax),
                        static_cast<const float*>(a.Z), a.ldz, static_cast<const float*>(a.ztgt), targets,
                        p.ignore_index, scale, K, logp, entropy, lse, top_ids, top_logp, status);
   note_launch(VCE_K_SCORE_MERGE, st);

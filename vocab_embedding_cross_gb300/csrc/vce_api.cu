@@ -641,11 +641,7 @@ vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, c
   if (!ws || !aligned(ws, kWsAlign) || ws_bytes < score_ws_bytes(*p, n_top)) return VCE_ERR_WORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* b = static_cast<char*>(ws);
-  int32_t* status = dev_status;
-  if (!status) {
-    status = reinterpret_cast<int32_t*>(b);
-    if (cudaError_t me = cudaMemsetAsync(status, 0, sizeof(int32_t), st)) return cuda_status(me);
-  }
+  int32_t* status = dev_status;   // may be null: data errors then go unreported
   if (score_decodes(*p))
     return cuda_status(launch_score_decode(*p, h, W, targets, logit_scale, n_top, logp, entropy, lse, top_ids, top_logp,
                                            ws, status, st));
@@ -702,11 +698,7 @@ vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, c
   int64_t vc = bwd_chunk_cols(*p, use_parts ? ws_bytes - part_bytes : ws_bytes);
   if (vc < 256) return VCE_ERR_WORKSPACE;
   if (vc > (int64_t(1) << 21)) vc = int64_t(1) << 21;   // the fp32 kernels' grids count 64-column blocks in 16 bits
-  int32_t* status = dev_status;
-  if (!status) {
-    status = reinterpret_cast<int32_t*>(b);
-    if (cudaError_t me = cudaMemsetAsync(status, 0, sizeof(int32_t), st)) return cuda_status(me);
-  }
+  int32_t* status = dev_status;   // may be null: data errors then go unreported
   int32_t* dh_flags = use_parts ? reinterpret_cast<int32_t*>(b + kBwdHeader) : nullptr;
   void* G = b + kBwdHeader + (use_parts ? part_bytes : 0);
   const ProbDev pd = prob_dev(*p);
