@@ -397,9 +397,9 @@ def vce_wait_selftest(limit_ns: int, dev_status, stream=None) -> None:
 KERNEL_KINDS = ["embed_gather", "embed_sort", "embed_reduce", "tc_fwd", "tc_grad", "tc_dh", "tc_dw",
                 "merge", "loss_mean", "count_valid", "simt_fwd", "simt_grad", "sgemm", "wait_selftest",
                 "dh_reduce", "sampled_cand", "sampled_scatter", "tc_argmax", "argmax_merge", "simt_argmax",
-                "ngram_hash", "ngram_fwd", "embed_hdr", "dh_bf16", "embed_sort_cluster", "tc_logits", "score_rows",
+                "ngram_hash", "ngram_fwd", "embed_hdr", "dh_bf16", "embed_sort_cluster", "tc_score", "score_rows",
                 "tc_score_grad", "simt_logits", "simt_score_grad", "mask_rows", "norm_fwd", "norm_bwd", "norm_sum",
-                "score_decode", "score_merge"]
+                "score_decode", "score_merge", "score_lists", "score_zero"]
 
 
 def vce_launch_count() -> int:

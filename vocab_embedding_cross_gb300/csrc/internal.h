@@ -85,6 +85,19 @@ struct ScoreGrad {
   float scale;   // logits are scale * <h, W>
 };
 
+// Statistics and lists of alternatives of the tensor-core scores.
+struct ScoreLists {
+  float scale;
+  int K;
+  float4* part;        // [T, n_units]: m, S, U of the scaled logits
+  uint2* scratch;      // score_scratch_entries() list entries (logit, class)
+  uint32_t* slots;     // score_slot_words(T): ordered chunk maxima
+  uint32_t* bound;     // [T] ordered lower bound on the K-th largest logit
+  uint2* row_list;     // [T, row_cap]: (ordered logit, ~class), the halves of a key
+  int64_t row_cap;
+  int32_t* row_count;  // [T]
+};
+
 // Host-side argument rules shared by every entry point that takes a problem
 // (shapes, flags, dtype, the ignore value, 32-bit work-item numbering).
 vce_status check_problem(const vce_problem* p);
@@ -209,9 +222,15 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
                                 void* G, int g_ld, float* dH, bool dH_accumulate, void* dW, bool dW_accumulate,
                                 int32_t* dh_flags, int dh_parts, int32_t* status, cudaStream_t st,
                                 const ScoreGrad* sg = nullptr, bool dW_bf16 = false);
-// Z[T, V_real] (row stride ldz, a multiple of 4) = h W^T in fp32.
-cudaError_t launch_tc_logits(const vce_problem& p, const void* h, const void* W, float* Z, int64_t ldz,
-                             int32_t* status, cudaStream_t st);
+// Per (token, unit) statistics into sl.part, target logits into ztgt and, for
+// sl.K > 0, the lists that launch_score_lists takes the alternatives from;
+// sl.slots, sl.bound and sl.row_count must be zero.
+int64_t score_scratch_entries();
+int64_t score_slot_words(int64_t T);
+int64_t score_row_cap(const UnitGrid& ug, int K);
+cudaError_t launch_tc_score(const vce_problem& p, const UnitGrid& ug, const void* h, const void* W,
+                            const int64_t* targets, const ScoreLists& sl, float* ztgt, int32_t* status,
+                            cudaStream_t st);
 // Number of K parts for the dH GEMM of one column chunk (fills the waves of
 // the persistent grid); at most kMaxDhParts.
 constexpr int kMaxDhParts = 8;
@@ -234,16 +253,21 @@ cudaError_t launch_ngram_embed_fwd(const vce_problem& p, const int64_t* ids, con
 
 // Token scores (score.cu): the longest list of alternatives, and the launchers.
 constexpr int kMaxTop = 32;
-// Scores of `rows` rows of logits, token t0 + row each; see vce_logprob_fwd.
-cudaError_t launch_score_rows(const float* Z, int64_t ldz, int64_t rows, int V, int64_t t0, const int64_t* targets,
+// Scores of `rows` rows of logits; see vce_logprob_fwd.
+cudaError_t launch_score_rows(const float* Z, int64_t ldz, int64_t rows, int V, const int64_t* targets,
                               int64_t ignore_index, float scale, int K, float* logp, float* entropy, float* lse,
                               int64_t* top_ids, float* top_logp, int32_t* status, cudaStream_t st);
+// The same from the tensor-core scores' statistics and lists.
+cudaError_t launch_score_lists(const ScoreLists& sl, int64_t T, int V, int n_units, const float* ztgt,
+                               const int64_t* targets, int64_t ignore_index, float* logp, float* entropy, float* lse,
+                               int64_t* top_ids, float* top_logp, int32_t* status, cudaStream_t st);
 // The same from h and W for at most kDecodeTokens tokens (bf16; score_decode.cu).
 constexpr int64_t kDecodeTokens = 128;
 size_t score_decode_ws_bytes(const vce_problem& p, int K);
 cudaError_t launch_score_decode(const vce_problem& p, const void* h, const void* W, const int64_t* targets,
                                 float scale, int K, float* logp, float* entropy, float* lse, int64_t* top_ids,
                                 float* top_logp, void* ws, int32_t* status, cudaStream_t st);
+cudaError_t launch_zero_words(void* p, size_t bytes, cudaStream_t st);   // bytes: a multiple of 16
 // out = h with the rows of tokens without a real target set to zero.
 cudaError_t launch_mask_rows(const void* h, const int64_t* targets, int64_t T, int V, int64_t ignore_index,
                              int64_t row_bytes, void* out, int32_t* status, cudaStream_t st);

@@ -12,7 +12,8 @@
 //   DH    dH (+)= G W      (A = G K-major, B = W rows as an MN-major operand)
 //   DW    dW (+)= G^T h    (A = G^T and B = h, both MN-major operands)
 // and the token scores' (log probabilities, entropy, top alternatives):
-//   LOGITS z = h W^T stored in fp32
+//   SCORE  FWD's items with U = sum exp(l - m) (l - m) beside the sum of exp,
+//          and lists of the logits that may be among a token's largest
 //   SGRAD  z recomputed; the epilogue forms the scores' gradient with respect
 //          to the logits in bf16 (score_grad below)
 //   DWB    DW with a bf16 result
@@ -41,6 +42,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "score.cuh"
 
 namespace vce {
 namespace {
@@ -59,24 +61,23 @@ constexpr uint32_t kAtomBytes = 64 * 128;        // 64 rows of 128 B: one MN-maj
 constexpr uint32_t kStagingPerWarp = 4096;       // one 32-row x 128-B TMA store box
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 enum Mode : int {
-  MODE_FWD = 0, MODE_GRAD = 1, MODE_DH = 2, MODE_DW = 3, MODE_ARGMAX = 4, MODE_LOGITS = 5, MODE_SGRAD = 6, MODE_DWB = 7
+  MODE_FWD = 0, MODE_GRAD = 1, MODE_DH = 2, MODE_DW = 3, MODE_ARGMAX = 4, MODE_SCORE = 5, MODE_SGRAD = 6, MODE_DWB = 7
 };
-// FWD and ARGMAX share the logit GEMM and its work items; they differ in the epilogue.
+// FWD, ARGMAX and SCORE share the logit GEMM and its work items; they differ in the epilogue.
 template <int MODE>
-constexpr bool kFwdLike = MODE == MODE_FWD || MODE == MODE_ARGMAX;
-// GRAD, SGRAD and LOGITS work on single 256 x 256 logit tiles of one column chunk.
-template <int MODE>
-constexpr bool kTileLike = MODE == MODE_GRAD || MODE == MODE_SGRAD || MODE == MODE_LOGITS;
-// GRAD and SGRAD store a bf16 gradient tile and precede a DH launch.
+constexpr bool kFwdLike = MODE == MODE_FWD || MODE == MODE_ARGMAX || MODE == MODE_SCORE;
+// GRAD and SGRAD work on single 256 x 256 logit tiles of one column chunk,
+// store a bf16 gradient tile and precede a DH launch.
 template <int MODE>
 constexpr bool kGradLike = MODE == MODE_GRAD || MODE == MODE_SGRAD;
 template <int MODE>
 constexpr bool kDwLike = MODE == MODE_DW || MODE == MODE_DWB;
 constexpr int kernel_kind(int mode) {
   return mode == MODE_ARGMAX   ? VCE_K_TC_ARGMAX
-         : mode == MODE_LOGITS ? VCE_K_TC_LOGITS
+         : mode == MODE_SCORE  ? VCE_K_TC_SCORE
          : mode == MODE_SGRAD  ? VCE_K_TC_SCORE_GRAD
          : mode == MODE_DWB    ? VCE_K_TC_DW
                                : VCE_K_TC_FWD + mode;
@@ -124,6 +125,7 @@ struct TcArgs {
   uint64_t limit_ns;
   int32_t* merge_ctr;   // FWD: the merge's block counter, zeroed here for the merge that follows
   ScoreGrad sg;         // SGRAD: what the forward scores left and their upstream gradients
+  ScoreLists sl;        // SCORE: statistics, scale and the lists of alternatives
 };
 
 // Items of the forward-like modes and of GRAD are (token block m, column
@@ -183,7 +185,7 @@ __device__ __forceinline__ TileCoord tile_coord(const TcArgs& a, int item, int t
     const UnitSpan us = unit_span(a, mc.c);
     c.am = mc.m * BMP + rank * BM;
     c.bn = static_cast<int32_t>(us.vb + static_cast<int64_t>(tt) * BN) + rank * BNH;
-  } else if constexpr (kTileLike<MODE>) {
+  } else if constexpr (kGradLike<MODE>) {
     const MC mc = item_mc(item, a.gm, a.n_mblk, a.n_cols);
     c.am = mc.m * BMP + rank * BM;
     c.bn = a.v0 + mc.c * BN + rank * BNH;
@@ -218,7 +220,7 @@ template <int MODE>
 __device__ __forceinline__ void issue_loads(const TcArgs& a, const CUtensorMap* mA, const CUtensorMap* mB,
                                             uint32_t sA, uint32_t sB, uint32_t bar, TileCoord c, int kb) {
   const int k0 = kb * BK;
-  if constexpr (kFwdLike<MODE> || kTileLike<MODE>) {
+  if constexpr (kFwdLike<MODE> || kGradLike<MODE>) {
     tma_load_2d_pair(sA, mA, bar, k0, c.am);
     tma_load_2d_pair(sB, mB, bar, k0, c.bn);
   } else if constexpr (MODE == MODE_DH) {
@@ -285,6 +287,139 @@ __device__ __forceinline__ ScoreGradRow score_grad_row(const ScoreGrad& g, int t
 __device__ __forceinline__ float score_grad(const ScoreGradRow& r, float z) {
   const float lp = fmaf(z, r.s, -r.lse);
   return ex2_approx(lp * kLog2e) * fmaf(lp + r.ent, r.c1, r.c0);
+}
+
+// Lists of alternatives (SCORE). Every epilogue thread appends the logits of its
+// row and column half that reach its threshold to a list in scratch memory
+// (entry i of lane l at i * 32 + l: a warp appending in step writes whole
+// lines). The threshold is the larger of two lower bounds on the row's K-th
+// largest logit:
+//   - the row's bound in global memory. 64 slots a row hold the maxima of the
+//     column groups counted into them by any CTA, every column into one slot;
+//     K slots' elements are at least as large as the K-th largest slot, which a
+//     thread of the row works out now and then (slot_bound). An element equal to
+//     it may still be one of the K, so it is kept. While a row has no bound, the
+//     tile is read twice: once to count its 8-column groups, which with those of
+//     the other CTAs at work make a first bound, and then for its entries;
+//   - the least element kept by the list's own last cut: K elements or more of
+//     lower columns are at least that large, so an equal one is not kept.
+// About 64 ln(64 / (64 - K)) logits seen so far reach the row's bound (24 for 20
+// alternatives; the least of K slots would let 61 through), so a row appends a
+// hundred or two of 150000 and most chunks have no hit in any of a warp's rows.
+// A list that grows long first drops what the bound has overtaken, each lane its
+// own entries; one that is still too long is cut by the whole warp to between K
+// and K + 16 entries, found by bisecting the keys. Cuts are left to rows whose
+// logits ascend with the class (one every 150 to 200 of them) and to the first
+// tiles. Thresholds only decide which losers are left out, so timing never
+// changes a result. At a unit's end the list's entries go to the row's own list.
+constexpr int kListCap = 256;    // entries, two tiles of a row's half; a chunk appends up to 32
+constexpr int kListSlack = 16;   // a cut leaves at most K + kListSlack
+constexpr int kSlots = 64;       // per row (at least kMaxTop)
+
+// Each lane's (n as bits, thr) after the lists of the lanes with `need` were cut.
+__device__ __noinline__ float2 cut_lists(uint2* base, int K, bool need, int n, float thr) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  unsigned todo = __ballot_sync(0xffffffffu, need);
+  __syncwarp();
+  while (todo) {
+    const int l = __ffs(todo) - 1;
+    todo &= todo - 1;
+    const int nl = __shfl_sync(0xffffffffu, n, l);
+    uint64_t key[kListCap / 32];
+    uint32_t top = 0, low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < kListCap / 32; ++j) {
+      const int i = lane + 32 * j;
+      key[j] = 0;
+      if (i < nl) {
+        const uint2 v = base[i * 32 + l];
+        const uint32_t o = ordered_bits(__uint_as_float(v.x));
+        key[j] = (static_cast<uint64_t>(o) << 32) | (0xFFFFFFFFu - v.y);
+        top = max(top, o);
+        low = min(low, o);
+      }
+    }
+    // largest bound that K keys reach, or any that at most K + kListSlack do
+    uint64_t lo = static_cast<uint64_t>(__reduce_min_sync(0xffffffffu, low)) << 32;
+    uint64_t hi = (static_cast<uint64_t>(__reduce_max_sync(0xffffffffu, top)) << 32) | 0xFFFFFFFFu;
+    int cnt = nl;
+    while (cnt > K + kListSlack && lo < hi) {
+      const uint64_t mid = lo + ((hi - lo) >> 1) + 1;
+      int c = 0;
+#pragma unroll
+      for (int j = 0; j < kListCap / 32; ++j) c += __popc(__ballot_sync(0xffffffffu, key[j] >= mid));
+      if (c >= K) {
+        lo = mid;
+        cnt = c;
+      } else {
+        hi = mid - 1;
+      }
+    }
+    int at = 0;
+    low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int j = 0; j < kListCap / 32; ++j) {
+      const bool keep = lane + 32 * j < nl && key[j] >= lo;
+      const unsigned who = __ballot_sync(0xffffffffu, keep);
+      if (keep) {
+        const uint32_t o = static_cast<uint32_t>(key[j] >> 32);
+        base[(at + __popc(who & ((1u << lane) - 1u))) * 32 + l] =
+            make_uint2(__float_as_uint(ordered_value(o)), 0xFFFFFFFFu - static_cast<uint32_t>(key[j]));
+        low = min(low, o);
+      }
+      at += __popc(who);
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    if (lane == l) {
+      n = at;
+      if (at >= K) thr = fmaxf(thr, ordered_value(low + 1));
+    }
+    __syncwarp();
+  }
+  return make_float2(__int_as_float(n), thr);
+}
+
+// Keeps the entries of this lane's list that reach the row's bound; returns how many.
+__device__ __noinline__ int sift_list(uint2* list, int n, float bound) {
+  int kept = 0;
+  for (int i = 0; i < n; i += 8) {
+    uint2 v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < n ? list[(i + j) * 32] : make_uint2(0, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n && __uint_as_float(v[j].x) >= bound) list[32 * kept++] = v[j];
+  }
+  return kept;
+}
+
+// A value that at least K of the row's slots reach, near their K-th largest
+// (the last 1/4096 of their range is not worth more steps); 0 while fewer than
+// K slots hold one.
+__device__ __noinline__ uint32_t slot_bound(const uint32_t* slots, int K) {
+  uint32_t v[kSlots], lo = 0xFFFFFFFFu, hi = 0;
+  int filled = 0;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) v[i] = __ldcg(slots + 32 * i);
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    if (v[i]) lo = min(lo, v[i]);
+    hi = max(hi, v[i]);
+    filled += v[i] ? 1 : 0;
+  }
+  if (filled < K) return 0;
+#pragma unroll 1
+  for (int step = 0; step < 12 && lo < hi; ++step) {
+    const uint32_t mid = lo + ((hi - lo) >> 1) + 1;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) c += v[i] >= mid ? 1 : 0;
+    if (c >= K)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
 }
 
 template <int MODE>
@@ -517,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
     };
     // One 32-row x 128-byte TMA store (or reduce-add) from this warp's staging box.
-    bool add_out = !kTileLike<MODE> && a.accumulate;
+    bool add_out = !kGradLike<MODE> && a.accumulate;
     auto store_box = [&](const uint32_t (&w)[32], int col, int row) {
       if (lane == 0) bulk_wait_read<0>();
       __syncwarp();
@@ -612,6 +747,208 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             i_run = oi;
           }
           if (t < a.pd.T) a.part[static_cast<int64_t>(t) * a.ug.n_units + u] = make_float2(m_run, __int_as_float(i_run));
+        }
+        ++items_done;
+      } else if constexpr (MODE == MODE_SCORE) {
+        const MC mc = item_mc(item, a.gm, a.n_mblk, a.n_cols);
+        const int u = mc.c;
+        const UnitSpan us = unit_span(a, u);
+        const int t = mc.m * BMP + static_cast<int>(rank) * BM + r;
+        const bool row_ok = t < a.pd.T;
+        const int64_t y = row_ok && a.targets ? a.targets[t] : -1;
+        const int K = a.sl.K;
+        const float sL = a.sl.scale * kLog2e;
+        float m_run = -INFINITY, s_run = 0.0f, u_run = 0.0f;   // of the unscaled maximum; sums in base 2
+        float thr = row_ok && K ? -INFINITY : INFINITY;
+        int n = 0;
+        uint2* list = K ? a.sl.scratch + static_cast<int64_t>(blockIdx.x * kEpiWarps + e) * (kListCap * 32) : nullptr;
+        // the row's slots, [T/32][kSlots][32], and bound
+        uint32_t* slots = K ? a.sl.slots + (static_cast<int64_t>(t >> 5) * (kSlots * 32) + (t & 31)) : nullptr;
+        const bool listed = row_ok && K;
+        float bound = -INFINITY;
+        auto refresh = [&] {
+          const uint32_t o = listed ? __ldcg(a.sl.bound + t) : 0;
+          if (o) bound = ordered_value(o);
+          thr = fmaxf(thr, bound);
+        };
+        auto raise_bound = [&] {
+          if (const uint32_t o = listed ? slot_bound(slots, K) : 0) atomicMax(a.sl.bound + t, o);
+        };
+        // Lists longer than `most` (K + kListSlack or more) are shortened to at most that.
+        auto shorten = [&](int most, bool must) {
+          if (!__any_sync(0xffffffffu, n > most)) return;
+          refresh();
+          if (n > most) n = sift_list(list + lane, n, bound);
+          if (!must || !__any_sync(0xffffffffu, n > most)) return;
+          const float2 v = cut_lists(list, K, n > most, n, thr);
+          n = __float_as_int(v.x);
+          thr = v.y;
+        };
+        int slot = 0;           // of the next chunk
+        bool counted = false;   // this tile's columns are in the slots already
+        auto chunk = [&](const uint32_t (&x)[32], int64_t vc0) {
+          const int64_t nval64 = us.vlim - vc0;
+          const int nval = nval64 >= 32 ? 32 : (nval64 <= 0 ? 0 : static_cast<int>(nval64));
+          if (nval == 0) return;
+          if (y >= vc0 && y < vc0 + nval) a.ztgt[t] = select32(x, static_cast<int>(y - vc0));
+          // maxima of eight columns each, then of the chunk
+          float gm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if (nval == 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) gm[j >> 3] = fmaxf(gm[j >> 3], __uint_as_float(x[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < nval) gm[j >> 3] = fmaxf(gm[j >> 3], __uint_as_float(x[j]));
+          }
+          const float cm = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
+          if (cm > m_run) {
+            const float d = m_run == -INFINITY ? 0.0f : (m_run - cm) * sL;   // nothing summed yet: 0 or NaN
+            const float c = ex2_approx(d);
+            u_run = c * fmaf(d, s_run, u_run);
+            s_run = c * s_run;
+            m_run = cm;
+          }
+          const float mL = m_run == -INFINITY ? 0.0f : m_run * sL;
+          float s0 = 0.0f, s1 = 0.0f, u0 = 0.0f, u1 = 0.0f;
+          // exp(-inf) * -inf is kept out by the clamp: 2^-300 is 0
+          if (nval == 32) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float d0 = fmaf(__uint_as_float(x[j]), sL, -mL), d1 = fmaf(__uint_as_float(x[j + 1]), sL, -mL);
+              const float e0 = ex2_approx(d0), e1 = ex2_approx(d1);
+              s0 += e0;
+              s1 += e1;
+              u0 = fmaf(e0, fmaxf(d0, -300.0f), u0);
+              u1 = fmaf(e1, fmaxf(d1, -300.0f), u1);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < nval) {
+                const float d0 = fmaf(__uint_as_float(x[j]), sL, -mL);
+                const float e0 = ex2_approx(d0);
+                s0 += e0;
+                u0 = fmaf(e0, fmaxf(d0, -300.0f), u0);
+              }
+          }
+          s_run += s0 + s1;
+          u_run += u0 + u1;
+          if (!K) return;
+          const bool hit = cm >= thr;
+          if (hit && !counted) atomicMax(slots + 32 * slot, ordered_bits(cm));
+          slot = (slot + 1) & (kSlots - 1);
+          if (__any_sync(0xffffffffu, hit)) {
+            shorten(kListCap - 32, true);
+            uint2* at = list + n * 32 + lane;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              if (!__any_sync(0xffffffffu, gm[g] >= thr)) continue;
+#pragma unroll
+              for (int j = 8 * g; j < 8 * g + 8; ++j) {
+                if (__uint_as_float(x[j]) >= thr && j < nval) {
+                  *at = make_uint2(x[j], static_cast<uint32_t>(vc0 + j));
+                  at += 32;
+                }
+              }
+            }
+            n = static_cast<int>(at - list) >> 5;
+          }
+        };
+        for (int tt = 0; tt < us.ntiles; ++tt) {
+          const uint32_t acc = tile_count & 1u;
+          refresh();
+          if (!mbar_wait_cl(&tfull[acc], (tile_count >> 1) & 1u, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int64_t vc = us.vb + static_cast<int64_t>(tt) * BN + half * 128;
+          const uint32_t ta = lane_base + acc * BN;
+          uint32_t xa[32], xb[32];
+          counted = false;
+          if (__any_sync(0xffffffffu, listed && bound == -INFINITY)) {
+            counted = tt == 0;
+            if (counted) {
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                tmem_ld_32x32b_x32(ta + 32 * c, xa);
+                tmem_ld_wait();
+                reg_fence(xa);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  float gm = -INFINITY;
+#pragma unroll
+                  for (int j = 8 * g; j < 8 * g + 8; ++j)
+                    if (vc + 32 * c + j < us.vlim) gm = fmaxf(gm, __uint_as_float(xa[j]));
+                  if (listed && vc + 32 * c + 8 * g < us.vlim)
+                    atomicMax(slots + 32 * ((u * 32 + half * 16 + c * 4 + g) & (kSlots - 1)), ordered_bits(gm));
+                }
+              }
+            }
+            raise_bound();
+            refresh();
+          } else if (half == 0 && tt == (us.ntiles >> 1)) {
+            raise_bound();
+          }
+          if (K) {
+            shorten(K + kListSlack, false);
+            slot = ((u * (a.ug.uw / BN) + tt) * 8 + half * 4) & (kSlots - 1);
+          }
+          tmem_ld_32x32b_x32(ta, xa);
+          tmem_ld_wait();
+          reg_fence(xa);
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            tmem_ld_32x32b_x32(ta + 64 * c + 32, xb);
+            chunk(xa, vc + 64 * c);
+            tmem_ld_wait();
+            reg_fence(xb);
+            if (c == 0) {
+              tmem_ld_32x32b_x32(ta + 64, xa);
+            } else {
+              release(acc);
+            }
+            chunk(xb, vc + 64 * c + 32);
+            tmem_ld_wait();
+            reg_fence(xa);
+          }
+          ++tile_count;
+        }
+        if (!ok) break;
+        if (K) {   // the unit's entries to the row's list
+          shorten(K + kListSlack, true);
+          if (n > 0) {
+            uint2* to = a.sl.row_list + static_cast<int64_t>(t) * a.sl.row_cap + atomicAdd(a.sl.row_count + t, n);
+            for (int i = 0; i < n; ++i) {
+              const uint2 v = list[i * 32 + lane];
+              to[i] = make_uint2(ordered_bits(__uint_as_float(v.x)), 0xFFFFFFFFu - v.y);
+            }
+          }
+          __syncwarp();
+        }
+        // Join the two half-row partials of the warps sharing this lane quarter.
+        if (half == 1) {
+          if (!mbar_wait(&comb_empty[pq], (items_done & 1u) ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          comb[pq * 32 + lane] = make_float4(m_run, s_run, u_run, 0.0f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&comb_full[pq]);
+        } else {
+          if (!mbar_wait(&comb_full[pq], items_done & 1u, wc)) {
+            ok = false;
+            break;
+          }
+          const float4 o = comb[pq * 32 + lane];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&comb_empty[pq]);
+          if (row_ok) {
+            const ScoreStat j = score_stat_join(ScoreStat{m_run * a.sl.scale, s_run, u_run * kLn2},
+                                                ScoreStat{o.x * a.sl.scale, o.y, o.z * kLn2});
+            a.sl.part[static_cast<int64_t>(t) * a.ug.n_units + u] = make_float4(j.m, j.S, j.U, 0.0f);
+          }
         }
         ++items_done;
       } else if constexpr (MODE == MODE_FWD) {
@@ -721,7 +1058,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ++items_done;
       } else {
         int m_blk, n_blk, row0, col0, part = 0;
-        if constexpr (kTileLike<MODE>) {
+        if constexpr (kGradLike<MODE>) {
           const MC mc = item_mc(item, a.gm, a.n_mblk, a.n_cols);
           m_blk = mc.m;
           n_blk = mc.c;
@@ -1114,21 +1451,30 @@ cudaError_t launch_tc_argmax(const vce_problem& p, const UnitGrid& ug, const voi
   return launch_mode<MODE_ARGMAX>(mh, mw, mh, a, st);
 }
 
-cudaError_t launch_tc_logits(const vce_problem& p, const void* h, const void* W, float* Z, int64_t ldz,
-                             int32_t* status, cudaStream_t st) {
-  CUtensorMap mh, mw, mz;
+int64_t score_scratch_entries() {
+  return static_cast<int64_t>(current_device_info().num_sms) * kEpiWarps * kListCap * 32;
+}
+int64_t score_row_cap(const UnitGrid& ug, int K) { return static_cast<int64_t>(ug.n_units) * 2 * (K + kListSlack); }
+
+int64_t score_slot_words(int64_t T) { return ceil_div(T, 32) * 32 * kSlots; }
+
+cudaError_t launch_tc_score(const vce_problem& p, const UnitGrid& ug, const void* h, const void* W,
+                            const int64_t* targets, const ScoreLists& sl, float* ztgt, int32_t* status,
+                            cudaStream_t st) {
+  CUtensorMap mh, mw;
   if (!make_tmap_2d(&mh, h, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.T, p.H, 64, BM, true) ||
-      !make_tmap_2d(&mw, W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.V_real, p.H, 64, BNH, true) ||
-      !make_tmap_2d(&mz, Z, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.V_real, p.T, ldz, 32, 32, true))
+      !make_tmap_2d(&mw, W, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.H, p.V_real, p.H, 64, BNH, true))
     return cudaErrorInvalidValue;
-  TcArgs a = base_args(p, nullptr, status);
+  TcArgs a = base_args(p, targets, status);
   a.n_mblk = static_cast<int>(ceil_div(p.T, BMP));
-  a.n_nblk = static_cast<int>(ceil_div(p.V_real, BN));
-  a.n_items = a.n_mblk * a.n_nblk;
+  a.n_items = a.n_mblk * ug.n_units;
   a.gm = tc_group_mblk(p);
-  a.n_cols = a.n_nblk;
+  a.n_cols = ug.n_units;
   a.num_kb = static_cast<int>(ceil_div(p.H, BK));
-  return launch_mode<MODE_LOGITS>(mh, mw, mz, a, st);
+  a.ug = ug;
+  a.ztgt = ztgt;
+  a.sl = sl;
+  return launch_mode<MODE_SCORE>(mh, mw, mh, a, st);
 }
 
 cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void* W, const int64_t* targets,

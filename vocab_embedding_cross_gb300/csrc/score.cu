@@ -24,126 +24,91 @@ namespace vce {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kRowCand = 1024;   // candidates kept in shared memory
+constexpr int kListThreads = 128;
 
-// One block per row of logits. First pass: running (m, S, U) and the largest
-// key of each thread's columns. The K-th largest of the 256 thread maxima
-// bounds the K-th largest key of the row from below, since they are K distinct
-// elements of it; the second pass collects what reaches the bound and ranks it
-// by counting. Rows where more than kRowCand keys reach the bound (their
-// largest logits all in a few threads' columns) take K scans instead.
+// One block per row of logits (the fp32 path): the statistics and, for
+// alternatives, the largest key of each thread's classes in a first pass over
+// the row, then the keys that reach the bound.
 __global__ void __launch_bounds__(kRowThreads)
-    score_rows_kernel(const float* __restrict__ Z, int64_t ldz, int V, int64_t t0, const int64_t* __restrict__ targets,
+    score_rows_kernel(const float* __restrict__ Z, int64_t ldz, int V, const int64_t* __restrict__ targets,
                       int64_t ignore_index, float scale, int K, float* __restrict__ logp, float* __restrict__ entropy,
                       float* __restrict__ lse, int64_t* __restrict__ top_ids, float* __restrict__ top_logp,
                       int32_t* status) {
-  __shared__ float sm[kRowThreads / 32], sS[kRowThreads / 32], sU[kRowThreads / 32];
-  __shared__ uint64_t skey[kRowThreads];
-  __shared__ uint64_t cand[kRowCand];
-  __shared__ uint64_t best[kMaxTop];
-  __shared__ uint64_t s_bound;
-  __shared__ int s_n;
+  __shared__ TopShared top;
+  __shared__ ScoreStat sh[32];
   grid_dep_launch();
+  top_init(top);
   grid_dep_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float* z = Z + static_cast<int64_t>(blockIdx.x) * ldz;
-  const int64_t t = t0 + blockIdx.x;
-  const uint32_t Vu = static_cast<uint32_t>(V);
+  const int64_t t = blockIdx.x;
+  const uint32_t n = static_cast<uint32_t>(V);
   ScoreStat a = score_stat_empty();
   uint64_t kmax = 0;
-  for (uint32_t v = 4 * tid; v < Vu; v += 4 * kRowThreads) {
-    const float4 q = *reinterpret_cast<const float4*>(z + v);   // rows are padded to a multiple of 4
-    const float x[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (v + j < Vu) {
-        score_stat_add(a, x[j] * scale);
-        const uint64_t k = top_key(x[j], v + j);
-        kmax = k > kmax ? k : kmax;
-      }
-    }
+  for (uint32_t v = threadIdx.x; v < n; v += kRowThreads) {
+    const float x = z[v];
+    score_stat_add(a, x * scale);
+    const uint64_t k = top_key(x, v);
+    kmax = k > kmax ? k : kmax;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    ScoreStat b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.S, o),
-                __shfl_xor_sync(0xffffffffu, a.U, o)};
-    a = (lane & o) == 0 ? score_stat_join(a, b) : score_stat_join(b, a);
-  }
-  if (lane == 0) {
-    sm[warp] = a.m;
-    sS[warp] = a.S;
-    sU[warp] = a.U;
-  }
-  skey[tid] = kmax;
-  if (tid == 0) {
-    s_n = 0;
-    s_bound = 0;
-  }
-  __syncthreads();
-  a = ScoreStat{sm[0], sS[0], sU[0]};
-  for (int w = 1; w < kRowThreads / 32; ++w) a = score_stat_join(a, ScoreStat{sm[w], sS[w], sU[w]});
+  if (K) top_raise(top, kmax);
+  a = block_join(a, sh);
   const float l = score_lse(a);
-  if (tid == 0) {
-    if (lse) lse[t] = l;
+  if (threadIdx.x == 0) {
     const int64_t y = targets ? targets[t] : -1;
-    const bool valid = targets && y >= 0 && y < V;
-    if (targets && !valid && y != ignore_index && status) atomicCAS(status, 0, static_cast<int>(VCE_ERR_BAD_INDEX));
-    if (logp) logp[t] = valid ? fmaf(z[y], scale, -l) : 0.0f;
-    if (entropy) entropy[t] = (!targets || valid) ? score_entropy(a) : 0.0f;
+    write_scores(a, l, t, V, targets, ignore_index, z + (y >= 0 && y < V ? y : 0), scale, logp, entropy, lse, status);
   }
   if (K == 0) return;
-  int rank = 0;
-  if (kmax)
-    for (int i = 0; i < kRowThreads; ++i) rank += skey[i] > kmax ? 1 : 0;
-  if (kmax && rank == K - 1) s_bound = kmax;   // stays 0 when fewer than K threads hold a key
-  if (tid < K) best[tid] = 0;
-  __syncthreads();
-  const uint64_t bound = s_bound;
-  for (uint32_t v = 4 * tid; v < Vu; v += 4 * kRowThreads) {
-    const float4 q = *reinterpret_cast<const float4*>(z + v);
-    const float x[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t k = v + j < Vu ? top_key(x[j], v + j) : 0;
-      if (k != 0 && k >= bound) {
-        const int at = atomicAdd(&s_n, 1);
-        if (at < kRowCand) cand[at] = k;
-      }
-    }
+  const uint64_t bound = top_bound(top, K);
+  for (uint32_t v = threadIdx.x; v < n; v += kRowThreads) top_collect(top, top_key(z[v], v), bound);
+  if (!top_rank(top, K)) top_scan(top, n, K, [&](uint32_t v) { return top_key(z[v], v); });
+  if (threadIdx.x < K) write_top(top.best[threadIdx.x], t * K + threadIdx.x, scale, l, top_ids, top_logp);
+}
+
+// One block per token: joins the tensor-core scores' unit statistics and takes
+// the alternatives from the row's list, which holds every logit that can be one.
+__global__ void __launch_bounds__(kListThreads)
+    score_lists_kernel(ScoreLists sl, int V, int n_units, const float* __restrict__ ztgt,
+                       const int64_t* __restrict__ targets, int64_t ignore_index, float* __restrict__ logp,
+                       float* __restrict__ entropy, float* __restrict__ lse, int64_t* __restrict__ top_ids,
+                       float* __restrict__ top_logp, int32_t* status) {
+  __shared__ TopShared top;
+  __shared__ ScoreStat sh[32];
+  grid_dep_launch();
+  top_init(top);
+  grid_dep_wait();
+  const int64_t t = blockIdx.x;
+  const int K = sl.K;
+  ScoreStat a = score_stat_empty();
+  for (int i = threadIdx.x; i < n_units; i += kListThreads) {
+    const float4 p = sl.part[t * n_units + i];
+    a = score_stat_join(a, ScoreStat{p.x, p.y, p.z});
   }
-  __syncthreads();
-  const int n = s_n;
-  if (n <= kRowCand) {
-    for (int i = tid; i < n; i += kRowThreads) {
-      const uint64_t k = cand[i];
-      int r = 0;
-      for (int j = 0; j < n; ++j) r += cand[j] > k ? 1 : 0;
-      if (r < K) best[r] = k;
-    }
-    __syncthreads();
-  } else {
-    uint64_t below = ~uint64_t(0);
-    for (int i = 0; i < K; ++i) {   // the largest key below the last one taken
-      uint64_t k = 0;
-      for (uint32_t v = tid; v < Vu; v += kRowThreads) {
-        const uint64_t kv = top_key(z[v], v);
-        if (kv < below && kv > k) k = kv;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t k2 = __shfl_xor_sync(0xffffffffu, k, o);
-        k = k2 > k ? k2 : k;
-      }
-      __syncthreads();
-      if (lane == 0) skey[warp] = k;
-      __syncthreads();
-      below = skey[0];
-      for (int w = 1; w < kRowThreads / 32; ++w) below = skey[w] > below ? skey[w] : below;
-      if (tid == 0) best[i] = below;
-    }
-    __syncthreads();
+  const uint32_t n = K ? static_cast<uint32_t>(sl.row_count[t]) : 0;
+  const uint2* list = sl.row_list + t * sl.row_cap;
+  auto key_at = [&](uint32_t i) { return (static_cast<uint64_t>(list[i].x) << 32) | list[i].y; };
+  uint64_t kmax = 0;
+  for (uint32_t i = threadIdx.x; i < n; i += kListThreads) {
+    const uint64_t k = key_at(i);
+    kmax = k > kmax ? k : kmax;
   }
-  if (tid < K) write_top(best[tid], t * K + tid, scale, l, top_ids, top_logp);
+  if (K) top_raise(top, kmax);
+  a = block_join(a, sh);
+  const float l = score_lse(a);
+  if (threadIdx.x == 0) write_scores(a, l, t, V, targets, ignore_index, ztgt + t, sl.scale, logp, entropy, lse, status);
+  if (K == 0) return;
+  const uint64_t bound = top_bound(top, K);
+  for (uint32_t i = threadIdx.x; i < n; i += kListThreads) top_collect(top, key_at(i), bound);
+  if (!top_rank(top, K)) top_scan(top, n, K, key_at);
+  if (threadIdx.x < K) write_top(top.best[threadIdx.x], t * K + threadIdx.x, sl.scale, l, top_ids, top_logp);
+}
+
+// Zeroes n words (a kernel and not a memset: the kernel after it can set itself up meanwhile).
+__global__ void __launch_bounds__(256) zero_words_kernel(uint4* __restrict__ p, int64_t n16) {
+  grid_dep_launch();
+  grid_dep_wait();
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n16;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+    p[i] = make_uint4(0, 0, 0, 0);
 }
 
 // Rows of h whose token takes part in the gradient, zeros for the others: the
@@ -166,13 +131,32 @@ __global__ void __launch_bounds__(256) mask_rows_kernel(const uint4* __restrict_
 
 }  // namespace
 
-cudaError_t launch_score_rows(const float* Z, int64_t ldz, int64_t rows, int V, int64_t t0, const int64_t* targets,
+cudaError_t launch_score_rows(const float* Z, int64_t ldz, int64_t rows, int V, const int64_t* targets,
                               int64_t ignore_index, float scale, int K, float* logp, float* entropy, float* lse,
                               int64_t* top_ids, float* top_logp, int32_t* status, cudaStream_t st) {
   const cudaError_t e = launch_dependent(score_rows_kernel, dim3(static_cast<unsigned>(rows)), dim3(kRowThreads), 0, st,
-                                         Z, ldz, V, t0, targets, ignore_index, scale, K, logp, entropy, lse, top_ids,
+                                         Z, ldz, V, targets, ignore_index, scale, K, logp, entropy, lse, top_ids,
                                          top_logp, status);
   note_launch(VCE_K_SCORE_ROWS, st);
+  return e;
+}
+
+cudaError_t launch_score_lists(const ScoreLists& sl, int64_t T, int V, int n_units, const float* ztgt,
+                               const int64_t* targets, int64_t ignore_index, float* logp, float* entropy, float* lse,
+                               int64_t* top_ids, float* top_logp, int32_t* status, cudaStream_t st) {
+  const cudaError_t e = launch_dependent(score_lists_kernel, dim3(static_cast<unsigned>(T)), dim3(kListThreads), 0, st,
+                                         sl, V, n_units, ztgt, targets, ignore_index, logp, entropy, lse, top_ids,
+                                         top_logp, status);
+  note_launch(VCE_K_SCORE_LISTS, st);
+  return e;
+}
+
+cudaError_t launch_zero_words(void* p, size_t bytes, cudaStream_t st) {
+  const int64_t n16 = static_cast<int64_t>(bytes / 16), want = ceil_div(n16, 256);
+  const int64_t cap = static_cast<int64_t>(current_device_info().num_sms) * 4;
+  const cudaError_t e = launch_dependent(zero_words_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)),
+                                         dim3(256), 0, st, static_cast<uint4*>(p), n16);
+  note_launch(VCE_K_SCORE_ZERO, st);
   return e;
 }
 

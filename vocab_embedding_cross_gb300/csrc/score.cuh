@@ -5,6 +5,8 @@
 #include <cmath>
 #include <cstdint>
 
+#include "internal.h"
+
 namespace vce {
 
 // Maximum m, S = sum exp(l - m) and U = sum exp(l - m) (l - m) of part of a row.
@@ -59,6 +61,128 @@ __device__ __forceinline__ void write_top(uint64_t key, int64_t at, float scale,
   const bool have = key != 0;
   top_ids[at] = have ? static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(key)) : -1;
   top_logp[at] = have ? fmaf(ordered_value(static_cast<uint32_t>(key >> 32)), scale, -lse) : NAN;
+}
+
+// ---------------------------------------------------------------------------
+// The K largest of many distinct keys, by one block. All functions are called by
+// every thread of the block, which has at least kBoundLists threads.
+// ---------------------------------------------------------------------------
+constexpr int kBoundLists = 64;   // lists whose largest keys give the bound (at least kMaxTop)
+constexpr int kCandidates = 1024;
+
+struct TopShared {
+  unsigned long long list[kBoundLists];
+  unsigned long long cand[kCandidates];
+  unsigned long long best[kMaxTop];   // the answer, largest first, 0 past the last key
+  unsigned long long warp[32];
+  unsigned long long bound;
+  int n;
+};
+
+__device__ __forceinline__ void top_init(TopShared& s) {
+  if (threadIdx.x < kBoundLists) s.list[threadIdx.x] = 0;
+  if (threadIdx.x < kMaxTop) s.best[threadIdx.x] = 0;
+  if (threadIdx.x == 0) {
+    s.bound = 0;
+    s.n = 0;
+  }
+  __syncthreads();
+}
+
+// After each thread has raised its list (thread i: list i mod 64) to a key that
+// some element of its own part reaches: the K-th largest of the lists, which K
+// elements reach, or 0 when fewer than K lists hold a key.
+__device__ __forceinline__ void top_raise(TopShared& s, uint64_t key) {
+  if (key) atomicMax(&s.list[threadIdx.x & (kBoundLists - 1)], static_cast<unsigned long long>(key));
+}
+__device__ __forceinline__ uint64_t top_bound(TopShared& s, int K) {
+  __syncthreads();
+  if (threadIdx.x < kBoundLists) {
+    const uint64_t k = s.list[threadIdx.x];
+    int rank = 0;
+#pragma unroll 16
+    for (int i = 0; i < kBoundLists; ++i) rank += s.list[i] > k ? 1 : 0;
+    if (k && rank == K - 1) s.bound = k;
+  }
+  __syncthreads();
+  return s.bound;
+}
+__device__ __forceinline__ void top_collect(TopShared& s, uint64_t key, uint64_t bound) {
+  if (key != 0 && key >= bound) {
+    const int at = atomicAdd(&s.n, 1);
+    if (at < kCandidates) s.cand[at] = key;
+  }
+}
+// Ranks what was collected; false when it was too much to keep.
+__device__ __forceinline__ bool top_rank(TopShared& s, int K) {
+  __syncthreads();
+  const int n = s.n;
+  if (n > kCandidates) return false;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const uint64_t k = s.cand[i];
+    int r = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) r += s.cand[j] > k ? 1 : 0;
+    if (r < K) s.best[r] = k;
+  }
+  __syncthreads();
+  return true;
+}
+// K scans of all keys, each for the largest below the last one: for rows whose
+// largest keys crowd into a few threads' parts.
+template <typename KeyAt>
+__device__ void top_scan(TopShared& s, uint32_t n, int K, KeyAt key_at) {
+  uint64_t below = ~uint64_t(0);
+  for (int i = 0; i < K; ++i) {
+    uint64_t k = 0;
+    for (uint32_t v = threadIdx.x; v < n; v += blockDim.x) {
+      const uint64_t kv = key_at(v);
+      if (kv < below && kv > k) k = kv;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const uint64_t k2 = __shfl_xor_sync(0xffffffffu, k, o);
+      k = k2 > k ? k2 : k;
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s.warp[threadIdx.x >> 5] = k;
+    __syncthreads();
+    below = 0;
+    for (uint32_t w = 0; w < blockDim.x / 32; ++w) below = s.warp[w] > below ? s.warp[w] : below;
+    if (threadIdx.x == 0) s.best[i] = below;
+  }
+  __syncthreads();
+}
+
+// Joins the threads' statistics; every thread gets the same bits. `sh` has 32 entries.
+__device__ __forceinline__ ScoreStat block_join(ScoreStat a, ScoreStat* sh) {
+  const int lane = static_cast<int>(threadIdx.x & 31), warps = static_cast<int>(blockDim.x >> 5);
+  auto over_warp = [&] {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const ScoreStat b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.S, o),
+                        __shfl_xor_sync(0xffffffffu, a.U, o)};
+      a = (lane & o) == 0 ? score_stat_join(a, b) : score_stat_join(b, a);
+    }
+  };
+  over_warp();
+  if (lane == 0) sh[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = lane < warps ? sh[lane] : score_stat_empty();
+  over_warp();
+  return a;
+}
+
+// One token's lse, logp and entropy (any output may be null), by one thread.
+__device__ __forceinline__ void write_scores(const ScoreStat& a, float lse_t, int64_t t, int V, const int64_t* targets,
+                                             int64_t ignore_index, const float* z_target, float scale, float* logp,
+                                             float* entropy, float* lse, int32_t* status) {
+  const int64_t y = targets ? targets[t] : -1;
+  const bool valid = targets && y >= 0 && y < V;
+  if (targets && !valid && y != ignore_index && status) atomicCAS(status, 0, static_cast<int>(VCE_ERR_BAD_INDEX));
+  if (lse) lse[t] = lse_t;
+  if (logp) logp[t] = valid ? fmaf(*z_target, scale, -lse_t) : 0.0f;
+  if (entropy) entropy[t] = (!targets || valid) ? score_entropy(a) : 0.0f;
 }
 
 }  // namespace vce

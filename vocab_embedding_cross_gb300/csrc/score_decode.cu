@@ -417,8 +417,6 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
 }
 
 constexpr int kMergeThreads = 1024;
-constexpr int kMergeCand = 1024;
-constexpr int kMergeLists = 64;    // group lists whose maxima give the bound (at least kMaxTop)
 constexpr int kMergePick = 512;    // groups read for candidates
 constexpr int kMergeKeep = 3;      // quadruples of group maxima that each thread keeps in registers
 
@@ -435,25 +433,15 @@ __global__ void __launch_bounds__(kMergeThreads)
                        float scale, int K, float* __restrict__ logp, float* __restrict__ entropy,
                        float* __restrict__ lse, int64_t* __restrict__ top_ids, float* __restrict__ top_logp,
                        int32_t* status) {
-  constexpr int kWarps = kMergeThreads / 32;
-  static_assert(kWarps == 32, "one partial per lane");
-  __shared__ ScoreStat sstat[kWarps];
-  __shared__ uint64_t skey[kMergeLists];
-  __shared__ uint64_t cand[kMergeCand];
-  __shared__ uint64_t best[kMaxTop];
+  __shared__ TopShared top;
+  __shared__ ScoreStat sh[32];
   __shared__ int pick[kMergePick];
-  __shared__ uint64_t s_bound;
-  __shared__ int s_n, s_pick;
+  __shared__ int s_pick;
   grid_dep_launch();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int64_t t = blockIdx.x;
-  if (tid < kMaxTop) best[tid] = 0;
-  if (tid < kMergeLists) skey[tid] = 0;
-  if (tid == 0) {
-    s_n = s_pick = 0;
-    s_bound = 0;
-  }
-  __syncthreads();
+  if (tid == 0) s_pick = 0;
+  top_init(top);
   grid_dep_wait();
   ScoreStat a = score_stat_empty();
   for (int i = tid; i < n_part; i += kMergeThreads) {
@@ -461,70 +449,41 @@ __global__ void __launch_bounds__(kMergeThreads)
     a = score_stat_join(a, ScoreStat{p.x, p.y, p.z});
   }
   // Thread i reads group quadruples i, i + 1024, ...; the first kMergeKeep stay in registers.
-  uint64_t kmax = 0;
   const uint4* gm = K ? reinterpret_cast<const uint4*>(gmax + t * ldg) : nullptr;
-  const int quads = (groups + 3) >> 2;
-  auto low_key = [&](uint32_t g, int i) {   // 0 for a group of NaN alone, and past the last group
-    return g && i < groups ? (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(min(16 * i + 16, V) - 1)) : 0;
+  const int quads = K ? (groups + 3) >> 2 : 0;
+  auto low_key = [&](uint32_t g, int i) -> uint64_t {   // 0 for a group of NaN alone, and past the last group
+    if (!g || i >= groups) return 0;
+    return (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(min(16 * i + 16, V) - 1));
   };
-  auto high_key = [&](uint32_t g, int i) {
-    return g && i < groups ? (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(16 * i)) : 0;
+  auto high_key = [&](uint32_t g, int i) -> uint64_t {
+    if (!g || i >= groups) return 0;
+    return (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(16 * i));
+  };
+  uint64_t kmax = 0;
+  auto raise = [&](const uint4& g, int quad) {
+    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t k = low_key(w[j], 4 * quad + j);
+      kmax = k > kmax ? k : kmax;
+    }
   };
   uint4 keep[kMergeKeep];
-  if (K) {
-    auto raise = [&](const uint4& g, int quad) {
-      const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint64_t k = low_key(w[j], 4 * quad + j);
-        kmax = k > kmax ? k : kmax;
-      }
-    };
-#pragma unroll
-    for (int c = 0; c < kMergeKeep; ++c) {
-      const int quad = tid + c * kMergeThreads;
-      keep[c] = quad < quads ? gm[quad] : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int c = 0; c < kMergeKeep; ++c) raise(keep[c], tid + c * kMergeThreads);
-    for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) raise(gm[quad], quad);
-    atomicMax(reinterpret_cast<unsigned long long*>(&skey[tid & (kMergeLists - 1)]), static_cast<unsigned long long>(kmax));
+  for (int c = 0; c < kMergeKeep; ++c) {
+    const int quad = tid + c * kMergeThreads;
+    keep[c] = quad < quads ? gm[quad] : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    ScoreStat b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.S, o),
-                __shfl_xor_sync(0xffffffffu, a.U, o)};
-    a = (lane & o) == 0 ? score_stat_join(a, b) : score_stat_join(b, a);
-  }
-  if (lane == 0) sstat[warp] = a;
-  __syncthreads();
-  if (K && tid < kMergeLists) {
-    const uint64_t k = skey[tid];
-    int rank = 0;
-#pragma unroll 16
-    for (int i = 0; i < kMergeLists; ++i) rank += skey[i] > k ? 1 : 0;
-    if (k && rank == K - 1) s_bound = k;   // stays 0 when fewer than K lists hold a group
-  }
-  // every warp joins the 32 warps' statistics
-  a = sstat[lane];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    ScoreStat b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.S, o),
-                __shfl_xor_sync(0xffffffffu, a.U, o)};
-    a = (lane & o) == 0 ? score_stat_join(a, b) : score_stat_join(b, a);
-  }
+  for (int c = 0; c < kMergeKeep; ++c) raise(keep[c], tid + c * kMergeThreads);
+  for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) raise(gm[quad], quad);
+  if (K) top_raise(top, kmax);
+  a = block_join(a, sh);
   const float l = score_lse(a);
-  if (tid == kMergeThreads - 1) {
-    if (lse) lse[t] = l;
-    const int64_t y = targets ? targets[t] : -1;
-    const bool valid = targets && y >= 0 && y < V;
-    if (targets && !valid && y != ignore_index && status) atomicCAS(status, 0, static_cast<int>(VCE_ERR_BAD_INDEX));
-    if (logp) logp[t] = valid ? fmaf(ztgt[t], scale, -l) : 0.0f;
-    if (entropy) entropy[t] = (!targets || valid) ? score_entropy(a) : 0.0f;
-  }
+  if (tid == kMergeThreads - 1)
+    write_scores(a, l, t, V, targets, ignore_index, ztgt + t, scale, logp, entropy, lse, status);
   if (K == 0) return;
-  __syncthreads();
-  const uint64_t bound = s_bound;
+  const uint64_t bound = top_bound(top, K);
   const float* z = Z + t * ldz;
   auto choose = [&](const uint4& g, int quad) {
     const uint32_t w[4] = {g.x, g.y, g.z, g.w};
@@ -542,52 +501,14 @@ __global__ void __launch_bounds__(kMergeThreads)
   for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) choose(gm[quad], quad);
   __syncthreads();
   const int n_pick = s_pick;
-  if (n_pick <= kMergePick) {
+  if (n_pick <= kMergePick)
     for (int i = tid >> 4; i < n_pick; i += kMergeThreads / 16) {
-      const int v = 16 * pick[i] + (lane & 15);
-      const uint64_t k = v < V ? top_key(z[v], static_cast<uint32_t>(v)) : 0;
-      if (k != 0 && k >= bound) {
-        const int at = atomicAdd(&s_n, 1);
-        if (at < kMergeCand) cand[at] = k;
-      }
+      const int v = 16 * pick[i] + (tid & 15);
+      if (v < V) top_collect(top, top_key(z[v], static_cast<uint32_t>(v)), bound);
     }
-  }
-  __syncthreads();
-  const int n = s_n;
-  if (n_pick <= kMergePick && n <= kMergeCand) {
-    for (int i = tid; i < n; i += kMergeThreads) {
-      const uint64_t k = cand[i];
-      int r = 0;
-#pragma unroll 8
-      for (int j = 0; j < n; ++j) r += cand[j] > k ? 1 : 0;
-      if (r < K) best[r] = k;
-    }
-    __syncthreads();
-  } else {
-    // Too many reach the bound (the largest logits all in a few lists): K
-    // scans of the row, each for the largest key below the last.
-    uint64_t below = ~uint64_t(0);
-    for (int i = 0; i < K; ++i) {
-      uint64_t k = 0;
-      for (uint32_t v = tid; v < static_cast<uint32_t>(V); v += kMergeThreads) {
-        const uint64_t kv = top_key(z[v], v);
-        if (kv < below && kv > k) k = kv;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const uint64_t k2 = __shfl_xor_sync(0xffffffffu, k, o);
-        k = k2 > k ? k2 : k;
-      }
-      __syncthreads();
-      if (lane == 0) skey[warp] = k;
-      __syncthreads();
-      below = skey[0];
-      for (int w = 1; w < kWarps; ++w) below = skey[w] > below ? skey[w] : below;
-      if (tid == 0) best[i] = below;
-    }
-    __syncthreads();
-  }
-  if (tid < K) write_top(best[tid], t * K + tid, scale, l, top_ids, top_logp);
+  if (n_pick > kMergePick || !top_rank(top, K))
+    top_scan(top, static_cast<uint32_t>(V), K, [&](uint32_t v) { return top_key(z[v], v); });
+  if (tid < K) write_top(top.best[tid], t * K + tid, scale, l, top_ids, top_logp);
 }
 
 struct DecLayout {

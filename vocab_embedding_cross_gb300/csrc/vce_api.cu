@@ -201,18 +201,57 @@ size_t dh_acc_bytes(const vce_problem& p) {
 }
 
 // ----- token scores -----
-// Tokens whose logits are in the workspace at one time: at most 512 MiB of
-// them, in whole token blocks of the tensor-core kernels.
-int64_t score_rows_per_pass(const vce_problem& p) {
-  const int64_t cap = (int64_t(512) << 20) / (p.Vp * 4);
-  int64_t r = cap >= 256 ? cap / 256 * 256 : cap;
-  if (r < 1) r = 1;
-  return r < p.T ? r : p.T;
-}
+// fp32: the logits of a block of tokens are kept in the workspace. bf16: up to
+// kDecodeTokens tokens, the decode kernel's logits and statistics; above, the
+// tensor-core scores' unit statistics and lists.
 bool score_decodes(const vce_problem& p) { return p.dtype == VCE_BF16 && p.T <= kDecodeTokens; }
-size_t score_ws_bytes(const vce_problem& p, int K) {
+struct ScoreLayout {
+  size_t part, ztgt, slots, bound, row_count, scratch, row_list, total;   // slots up to scratch: zeroed
+  int64_t row_cap;
+  UnitGrid ug;
+};
+ScoreLayout score_layout(const vce_problem& p, int K) {
+  ScoreLayout L{};
+  L.ug = unit_grid(p, tc_unit_width(p));
+  L.row_cap = K ? score_row_cap(L.ug, K) : 0;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes, kWsAlign);
+    return o;
+  };
+  const size_t T = static_cast<size_t>(p.T);
+  L.part = take(T * L.ug.n_units * sizeof(float4));
+  L.ztgt = take(T * sizeof(float));
+  L.slots = take(K ? static_cast<size_t>(score_slot_words(p.T)) * sizeof(uint32_t) : 0);
+  L.bound = take(K ? T * sizeof(uint32_t) : 0);
+  L.row_count = take(K ? T * sizeof(int32_t) : 0);
+  L.scratch = take(K ? static_cast<size_t>(score_scratch_entries()) * sizeof(uint2) : 0);
+  L.row_list = take(K ? T * static_cast<size_t>(L.row_cap) * sizeof(uint2) : 0);
+  L.total = off;
+  return L;
+}
+size_t score_pass_bytes(const vce_problem& p, int K) {
   if (score_decodes(p)) return score_decode_ws_bytes(p, K);
-  return kWsAlign + align_up(static_cast<size_t>(score_rows_per_pass(p)) * static_cast<size_t>(p.Vp) * 4, kWsAlign);
+  if (p.dtype == VCE_BF16) return score_layout(p, K).total;
+  return align_up(static_cast<size_t>(p.T) * static_cast<size_t>(p.Vp) * 4, kWsAlign);
+}
+// Tokens per pass: all of them where a pass fits in 512 MiB, else whole token
+// blocks of the tensor-core kernels that do (one token at the least).
+int64_t score_rows_per_pass(const vce_problem& p, int K) {
+  constexpr size_t kCap = size_t(512) << 20;
+  vce_problem q = p;
+  while (q.T > 1 && score_pass_bytes(q, K) > kCap) q.T = q.T > 256 ? ceil_div(q.T, 512) * 256 : ceil_div(q.T, 2);
+  return q.T;
+}
+size_t score_ws_bytes(const vce_problem& p, int K) {
+  vce_problem q = p;
+  q.T = score_rows_per_pass(p, K);
+  // a shorter last pass may take the decode path
+  vce_problem r = p;
+  r.T = q.T > 0 ? p.T % q.T : 0;
+  const size_t a = score_pass_bytes(q, K), b = r.T > 0 ? score_pass_bytes(r, K) : 0;
+  return kWsAlign + (a > b ? a : b);
 }
 // The backward's copy of h without the rows of ignored tokens.
 size_t masked_h_bytes(const vce_problem& p) {
@@ -642,22 +681,44 @@ vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, c
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   char* b = static_cast<char*>(ws);
   int32_t* status = dev_status;   // may be null: data errors then go unreported
-  if (score_decodes(*p))
-    return cuda_status(launch_score_decode(*p, h, W, targets, logit_scale, n_top, logp, entropy, lse, top_ids, top_logp,
-                                           ws, status, st));
-  float* Z = reinterpret_cast<float*>(b + kWsAlign);
-  const int64_t rows = score_rows_per_pass(*p);
+  const int64_t rows = score_rows_per_pass(*p, n_top);
   for (int64_t t0 = 0; t0 < p->T; t0 += rows) {
     vce_problem q = *p;
     q.T = p->T - t0 < rows ? p->T - t0 : rows;
+    auto at = [&](auto* x) { return x ? x + t0 : x; };
     const char* hr = static_cast<const char*>(h) + static_cast<size_t>(t0) * p->H * esize_of(*p);
-    cudaError_t e = p->dtype == VCE_BF16
-                        ? launch_tc_logits(q, hr, W, Z, p->Vp, status, st)
-                        : launch_simt_logits(prob_dev(q), reinterpret_cast<const float*>(hr),
-                                             static_cast<const float*>(W), Z, p->Vp, st);
-    if (e == cudaSuccess)
-      e = launch_score_rows(Z, p->Vp, q.T, static_cast<int>(p->V_real), t0, targets, p->ignore_index, logit_scale,
-                            n_top, logp, entropy, lse, top_ids, top_logp, status, st);
+    int64_t* ids = n_top ? top_ids + t0 * n_top : nullptr;
+    float* tlp = n_top ? top_logp + t0 * n_top : nullptr;
+    const int V = static_cast<int>(p->V_real);
+    cudaError_t e;
+    if (score_decodes(q)) {
+      e = launch_score_decode(q, hr, W, at(targets), logit_scale, n_top, at(logp), at(entropy), at(lse), ids, tlp, b,
+                              status, st);
+    } else if (p->dtype == VCE_BF16) {
+      const ScoreLayout L = score_layout(q, n_top);
+      const ScoreLists sl{logit_scale,
+                          n_top,
+                          reinterpret_cast<float4*>(b + L.part),
+                          reinterpret_cast<uint2*>(b + L.scratch),
+                          reinterpret_cast<uint32_t*>(b + L.slots),
+                          reinterpret_cast<uint32_t*>(b + L.bound),
+                          reinterpret_cast<uint2*>(b + L.row_list),
+                          L.row_cap,
+                          reinterpret_cast<int32_t*>(b + L.row_count)};
+      float* ztgt = reinterpret_cast<float*>(b + L.ztgt);
+      e = n_top ? launch_zero_words(b + L.slots, L.scratch - L.slots, st) : cudaSuccess;
+      if (e == cudaSuccess) e = launch_tc_score(q, L.ug, hr, W, at(targets), sl, ztgt, status, st);
+      if (e == cudaSuccess)
+        e = launch_score_lists(sl, q.T, V, L.ug.n_units, ztgt, at(targets), p->ignore_index, at(logp), at(entropy),
+                               at(lse), ids, tlp, status, st);
+    } else {
+      float* Z = reinterpret_cast<float*>(b);
+      e = launch_simt_logits(prob_dev(q), reinterpret_cast<const float*>(hr), static_cast<const float*>(W), Z, p->Vp,
+                             st);
+      if (e == cudaSuccess)
+        e = launch_score_rows(Z, p->Vp, q.T, V, at(targets), p->ignore_index, logit_scale, n_top, at(logp),
+                              at(entropy), at(lse), ids, tlp, status, st);
+    }
     if (e != cudaSuccess) return cuda_status(e);
   }
   return VCE_OK;
