@@ -766,11 +766,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t* slots = K ? a.sl.slots + (static_cast<int64_t>(t >> 5) * (kSlots * 32) + (t & 31)) : nullptr;
         const bool listed = row_ok && K;
         float bound = -INFINITY;
-        auto refresh = [&] {
-          const uint32_t o = listed ? __ldcg(a.sl.bound + t) : 0;
+        // The bound is read at a tile's start for the next one, so that no warp waits for L2.
+        uint32_t next_bound = listed ? __ldcg(a.sl.bound + t) : 0;
+        auto take_bound = [&](uint32_t o) {
           if (o) bound = ordered_value(o);
           thr = fmaxf(thr, bound);
         };
+        auto refresh = [&] { take_bound(listed ? __ldcg(a.sl.bound + t) : 0); };
+        // Units come in ascending order; the bound moves as 1 / (classes seen), so
+        // units 0, 1, 2, 3, 4, 6, 8, 12, 16, 24, ... work it out anew.
+        const int below_top = u & (u - 1);
+        const bool raises = half == 0 && (below_top & (below_top - 1)) == 0;
         auto raise_bound = [&] {
           if (const uint32_t o = listed ? slot_bound(slots, K) : 0) atomicMax(a.sl.bound + t, o);
         };
@@ -840,29 +846,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           slot = (slot + 1) & (kSlots - 1);
           if (__any_sync(0xffffffffu, hit)) {
             shorten(kListCap - 32, true);
-            uint2* at = list + n * 32 + lane;
+            uint32_t at = static_cast<uint32_t>(n * 32 + lane) * 8u;
+            char* const to = reinterpret_cast<char*>(list);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               if (!__any_sync(0xffffffffu, gm[g] >= thr)) continue;
 #pragma unroll
               for (int j = 8 * g; j < 8 * g + 8; ++j) {
                 if (__uint_as_float(x[j]) >= thr && j < nval) {
-                  *at = make_uint2(x[j], static_cast<uint32_t>(vc0 + j));
-                  at += 32;
+                  *reinterpret_cast<uint2*>(to + at) = make_uint2(x[j], static_cast<uint32_t>(vc0) + j);
+                  at += 32 * 8;
                 }
               }
             }
-            n = static_cast<int>(at - list) >> 5;
+            n = static_cast<int>(at >> 8);
           }
         };
         for (int tt = 0; tt < us.ntiles; ++tt) {
           const uint32_t acc = tile_count & 1u;
-          refresh();
           if (!mbar_wait_cl(&tfull[acc], (tile_count >> 1) & 1u, wc)) {
             ok = false;
             break;
           }
           tc_fence_after();
+          take_bound(next_bound);
+          if (listed) next_bound = __ldcg(a.sl.bound + t);
           const int64_t vc = us.vb + static_cast<int64_t>(tt) * BN + half * 128;
           const uint32_t ta = lane_base + acc * BN;
           uint32_t xa[32], xb[32];
@@ -888,7 +896,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             raise_bound();
             refresh();
-          } else if (half == 0 && tt == (us.ntiles >> 1)) {
+          } else if (raises && tt == (us.ntiles >> 1)) {
             raise_bound();
           }
           if (K) {
