@@ -273,7 +273,6 @@ cudaError_t launch_mask_rows(const void* h, const int64_t* targets, int64_t T, i
                              int64_t row_bytes, void* out, int32_t* status, cudaStream_t st);
 
 // Layer and RMS normalisation (norm.cu).
-int norm_parts(const vce_problem& p);
 size_t norm_ws_bytes(const vce_problem& p);
 cudaError_t launch_norm_fwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* b, float eps,
                             void* y, float* mean, float* rstd, cudaStream_t st);
