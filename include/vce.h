@@ -399,7 +399,7 @@ vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, c
  */
 typedef enum vce_norm_kind { VCE_NORM_LAYER = 0, VCE_NORM_RMS = 1 } vce_norm_kind;
 vce_status vce_norm_fwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* bias,
-                        float eps, void* y, float* mean, float* rstd, void* stream);
+                        float eps, void* y, float* mean, float* rstd, int32_t* dev_status, void* stream);
 
 /*
  * Backward of vce_norm_fwd. dy[T,H] is the dH of vce_loss_bwd or
@@ -416,7 +416,7 @@ vce_status vce_norm_fwd(const vce_problem* p, int32_t kind, const void* x, const
  */
 vce_status vce_norm_bwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* dy,
                         const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
-                        int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+                        int32_t accumulate, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
 /*
  * Hashed n-gram input embeddings ["Sampled Softmax with Over-Tokenized

@@ -37,12 +37,12 @@ def bwd(L, p, h=FAKE, W=FAKE, y=FAKE, lse=FAKE, ent=FAKE, gl=FAKE, ge=FAKE, scal
 
 
 def nfwd(L, p, kind=0, x=FAKE, w=FAKE, b=FAKE, eps=1e-5, y=FAKE, mean=FAKE, rstd=FAKE):
-    return L.vce_norm_fwd(ctypes.byref(p), kind, x, w, b, eps, y, mean, rstd, None)
+    return L.vce_norm_fwd(ctypes.byref(p), kind, x, w, b, eps, y, mean, rstd, None, None)
 
 
 def nbwd(L, p, kind=0, x=FAKE, w=FAKE, dy=FAKE, mean=FAKE, rstd=FAKE, dx=FAKE, dw=FAKE, db=FAKE, acc=0, ws=FAKE,
          nb=1 << 40):
-    return L.vce_norm_bwd(ctypes.byref(p), kind, x, w, dy, mean, rstd, dx, dw, db, acc, ws, nb, None)
+    return L.vce_norm_bwd(ctypes.byref(p), kind, x, w, dy, mean, rstd, dx, dw, db, acc, ws, nb, None, None)
 
 
 @pytest.mark.parametrize("call", [fwd, bwd, nfwd, nbwd])

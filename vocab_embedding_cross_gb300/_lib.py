@@ -113,10 +113,10 @@ def lib():
                                       c_void_p, c_void_p, c_int32, c_void_p, c_size_t, c_void_p, c_void_p]
         L.vce_logprob_bwd.restype = c_int32
         L.vce_norm_fwd.argtypes = [P, c_int32, c_void_p, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_void_p,
-                                   c_void_p]
+                                   c_void_p, c_void_p]
         L.vce_norm_fwd.restype = c_int32
         L.vce_norm_bwd.argtypes = [P, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
-                                   c_void_p, c_int32, c_void_p, c_size_t, c_void_p]
+                                   c_void_p, c_int32, c_void_p, c_size_t, c_void_p, c_void_p]
         L.vce_norm_bwd.restype = c_int32
         L.vce_status_str.argtypes = [c_int32]
         L.vce_status_str.restype = ctypes.c_char_p
@@ -319,17 +319,18 @@ def vce_logprob_bwd(p, h, W, targets, lse, entropy, g_logp, g_entropy, dH, dW, w
            "vce_logprob_bwd")
 
 
-def vce_norm_fwd(p, x, weight, bias, y, mean=None, rstd=None, eps=1e-5, kind=VCE_NORM_LAYER, stream=None) -> None:
+def vce_norm_fwd(p, x, weight, bias, y, mean=None, rstd=None, eps=1e-5, kind=VCE_NORM_LAYER, dev_status=None,
+                 stream=None) -> None:
     import torch
     T, H, e, f32 = p.T, p.H, _elem(p), torch.float32
     _check(lib().vce_norm_fwd(ctypes.byref(p), int(kind), _arg(x, "x", e, (T, H)),
                               _arg(weight, "weight", e, (H,), True), _arg(bias, "bias", e, (H,), True), float(eps),
                               _arg(y, "y", e, (T, H)), _arg(mean, "mean", f32, (T,), True),
-                              _arg(rstd, "rstd", f32, (T,), True), _stream(stream)), "vce_norm_fwd")
+                              _arg(rstd, "rstd", f32, (T,), True), _ptr(dev_status), _stream(stream)), "vce_norm_fwd")
 
 
 def vce_norm_bwd(p, x, weight, dy, mean, rstd, dx, dweight, dbias, ws, kind=VCE_NORM_LAYER, accumulate=False,
-                 ws_bytes=None, stream=None) -> None:
+                 ws_bytes=None, dev_status=None, stream=None) -> None:
     import torch
     nb = ws.numel() * ws.element_size() if ws_bytes is None else ws_bytes
     T, H, e, f32 = p.T, p.H, _elem(p), torch.float32
@@ -338,7 +339,7 @@ def vce_norm_bwd(p, x, weight, dy, mean, rstd, dx, dweight, dbias, ws, kind=VCE_
                               _arg(mean, "mean", f32, (T,), True), _arg(rstd, "rstd", f32, (T,)),
                               _arg(dx, "dx", e, (T, H), True), _arg(dweight, "dweight", f32, (H,), True),
                               _arg(dbias, "dbias", f32, (H,), True), int(bool(accumulate)), _ptr(ws), nb,
-                              _stream(stream)), "vce_norm_bwd")
+                              _ptr(dev_status), _stream(stream)), "vce_norm_bwd")
 
 
 def vce_ngram_hash(ids, n, V, M, out, seq_len=0, stream=None) -> None:

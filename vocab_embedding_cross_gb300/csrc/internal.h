@@ -275,10 +275,10 @@ cudaError_t launch_mask_rows(const void* h, const int64_t* targets, int64_t T, i
 // Layer and RMS normalisation (norm.cu).
 size_t norm_ws_bytes(const vce_problem& p);
 cudaError_t launch_norm_fwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* b, float eps,
-                            void* y, float* mean, float* rstd, cudaStream_t st);
-cudaError_t launch_norm_bwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* dy, bool dy_bf16,
+                            void* y, float* mean, float* rstd, int32_t* status, cudaStream_t st);
+cudaError_t launch_norm_bwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* dy,
                             const float* mean, const float* rstd, void* dx, float* dw, float* db, bool accumulate,
-                            void* ws, cudaStream_t st);
+                            void* ws, int32_t* status, cudaStream_t st);
 
 // Sampled-softmax candidate list.
 size_t sampled_ws_bytes(const vce_problem& p);

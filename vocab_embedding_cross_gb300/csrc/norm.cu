@@ -10,9 +10,11 @@
 //
 // Both directions are bound by memory: x (and dy) once in, y (or dx) once out.
 // A row belongs to a group of 32 to 1024 threads that keeps it in registers
-// between the statistics and the output, so each byte moves once; the groups of
-// a persistent grid go through the rows with the next row's loads in flight
-// while a row is worked on. In the backward each thread's columns are the same
+// between the statistics and the output, so each byte moves once. The groups of
+// a persistent grid go through the rows; a ring of one to four rows a group is
+// filled by bulk copies, so that up to 200 KB are in flight on each SM however
+// few registers the threads have (with the next row fetched into registers
+// instead, 32 KB, the forward took 37 us for 16384 rows of 2048). In the backward each thread's columns are the same
 // for every row, so the weight gradients are summed in its registers over all
 // rows of the group and leave the CTA once, as one partial per CTA (2 H floats
 // for each of at most 152), which a second small kernel adds up.
@@ -23,6 +25,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace vce {
 namespace {
@@ -95,6 +98,16 @@ struct RowN {
   }
 };
 
+// A barrier of one group. Groups of several warps have the named barriers 1 to 15:
+// barrier 0 is the whole CTA's, which another group may already wait at with the
+// CTA's thread count.
+constexpr int kNamedBarriers = 15;
+__device__ __forceinline__ void group_sync(int id, int G) {
+  if (G == 32)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(G) : "memory");
+}
 // Sum over a group of G threads (a multiple of 32); every thread gets the same
 // bits. The two halves of `sh` are used in turn, so one barrier a sum is enough.
 struct GroupSum {
@@ -108,115 +121,180 @@ struct GroupSum {
     buf ^= 1;
     const int warp = static_cast<int>(threadIdx.x % G) >> 5;
     if ((threadIdx.x & 31) == 0) s[warp] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(G) : "memory");
+    group_sync(id, G);
     v = 0.0f;
     for (int w = 0; w < (G >> 5); ++w) v += s[w];
     return v;
   }
 };
 
-constexpr int kFwdThreads = 256;
+constexpr int kFwdThreads = 1024;
 constexpr int kBwdThreads = 512;
-constexpr int kMaxGroups = 16;   // of one CTA (named barriers 1 to 15 serve groups of two warps and more)
+constexpr int kMaxGroups = 32;
+constexpr int kMaxSlots = 4;
+constexpr uint32_t kRingBytes = 200 * 1024;
 
-// VPT vectors a thread. Up to two of them, the weights stay in registers over the
-// rows and the next row is fetched ahead (64 registers, so that 1024 threads of an
-// SM hold 32 KB of rows in flight); four (rows of over 2048 vectors) do without.
+// Copies `bytes` (a multiple of 16) into shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// A group's ring of rows. Row number it of the group is in slot it % slots; the
+// group's first thread refills a slot once the whole group has read it. Every
+// wait is bounded: a group whose wait runs out goes on without waiting, so that
+// none of its threads is left at a barrier, and its rows are not to be used
+// (VCE_ERR_TIMEOUT in the status word).
+struct RowRing {
+  uint64_t* full;
+  char* buf;
+  uint32_t slot_bytes;
+  int slots, slot, issued;
+  uint32_t phase;
+  bool ok, lead;
+  WaitCtx wc;
+  __device__ __forceinline__ char* wait() {
+    ok = ok && mbar_wait(&full[slot], phase, wc);
+    return buf + static_cast<size_t>(slot) * slot_bytes;
+  }
+  __device__ __forceinline__ void next() {
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+  // At the end of a group whose wait ran out: its copies land before the memory goes away.
+  __device__ void drain() {
+    if (ok || !lead) return;
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0; i < slots && i < issued; ++i) {
+      const uint32_t uses = static_cast<uint32_t>((issued - 1 - i) / slots);   // earlier uses of the slot
+      while (!mbar_try_wait(&full[i], uses & 1u) && globaltimer_ns() - t0 < 100000000ull) {
+      }
+    }
+  }
+};
+__device__ __forceinline__ RowRing make_ring(uint64_t (*full)[kMaxSlots], char* smem, int g, int slots,
+                                             uint32_t slot_bytes, bool lead, const WaitCtx& wc) {
+  if (lead) {
+    for (int i = 0; i < slots; ++i) mbar_init(&full[g][i], 1);
+    fence_mbar_init();
+  }
+  return RowRing{full[g], smem + static_cast<size_t>(g) * slots * slot_bytes, slot_bytes, slots, 0, 0, 0, true, lead, wc};
+}
+
+// VPT vectors of 16 bytes a thread (up to four), kept as they were stored.
 template <typename E, int VPT>
-__global__ void __launch_bounds__(1024)
-    norm_fwd_kernel(int64_t T, int H, int G, int rms, const E* __restrict__ x, const E* __restrict__ w,
+__global__ void __launch_bounds__(kFwdThreads)
+    norm_fwd_kernel(int64_t T, int H, int G, int slots, int rms, const E* __restrict__ x, const E* __restrict__ w,
                     const E* __restrict__ b, float eps, E* __restrict__ y, float* __restrict__ mean,
-                    float* __restrict__ rstd) {
+                    float* __restrict__ rstd, int32_t* status, uint64_t limit_ns) {
   constexpr int N = Row16<E>::N;
-  constexpr bool kAhead = VPT <= 2;
   __shared__ float sh[kMaxGroups][64];
+  __shared__ uint64_t full[kMaxGroups][kMaxSlots];
+  __shared__ int s_abort;
+  extern __shared__ __align__(16) char ring_mem[];
   grid_dep_launch();
-  grid_dep_wait();
   const int nv = H / N, groups = static_cast<int>(blockDim.x) / G;
   const int g = static_cast<int>(threadIdx.x) / G, i0 = static_cast<int>(threadIdx.x) % G;
+  if (threadIdx.x == 0) s_abort = 0;
+  RowRing ring = make_ring(full, ring_mem, g, slots, static_cast<uint32_t>(nv) * 16u, i0 == 0,
+                           WaitCtx{&s_abort, status, limit_ns});
+  __syncthreads();
+  grid_dep_wait();
   GroupSum sum{sh[g], G, 1 + g, 0};
   const float inv = 1.0f / static_cast<float>(H);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  Row16<E> wv[VPT], bv[VPT], xv[VPT];
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int i = i0 + j * G;
-    if (kAhead && i < nv && w) wv[j].load(w, i);
-    if (kAhead && i < nv && b) bv[j].load(b, i);
-  }
   int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
-  auto fetch = [&](int64_t row) {
+  auto fill = [&](int slot, int64_t row) {
+    if (!ring.lead || row >= T || !ring.ok) return;
+    mbar_arrive_expect_tx(&ring.full[slot], ring.slot_bytes);
+    bulk_load(ring.buf + static_cast<size_t>(slot) * ring.slot_bytes, x + row * H, ring.slot_bytes, &ring.full[slot]);
+    ++ring.issued;
+  };
+  for (int i = 0; i < slots; ++i) fill(i, t + i * step);
+  for (; t < T; t += step) {
+    const uint4* row = reinterpret_cast<const uint4*>(ring.wait());
+    Row16<E> xv[VPT];
+    float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
-      if (row < T && i0 + j * G < nv) xv[j].load(x, row * nv + i0 + j * G);
-  };
-  if (kAhead) fetch(t);
-  for (; t < T; t += step) {
-    float f[VPT][N];
-    float s = 0.0f;
-    if (!kAhead) fetch(t);
+      if (i0 + j * G < nv) {
+        xv[j].load(reinterpret_cast<const E*>(row), i0 + j * G);
+        float f[N];
+        xv[j].get(f);
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      if (i0 + j * G < nv) xv[j].get(f[j]);
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if (i0 + j * G >= nv) f[j][k] = 0.0f;
-        s += f[j][k];
+        for (int k = 0; k < N; ++k) s += f[k];
       }
-    }
-    if (kAhead) fetch(t + step);
     const float mu = rms ? 0.0f : sum(s) * inv;
     float q = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
+      if (i0 + j * G < nv) {
+        float f[N];
+        xv[j].get(f);
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        f[j][k] -= mu;
-        if (i0 + j * G < nv) q = fmaf(f[j][k], f[j][k], q);
+        for (int k = 0; k < N; ++k) q = fmaf(f[k] - mu, f[k] - mu, q);
       }
-    const float r = 1.0f / sqrtf(sum(q) * inv + eps);
+    const float r = 1.0f / sqrtf(sum(q) * inv + eps);   // the whole group has read the slot
+    fill(ring.slot, t + slots * step);
+    ring.next();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int i = i0 + j * G;
       if (i >= nv) continue;
-      float c[N];
-      if (!kAhead && w) wv[j].load(w, i);
-      if (!kAhead && b) bv[j].load(b, i);
-      if (w) wv[j].get(c);
+      float f[N], c[N];
+      Row16<E> v;
+      xv[j].get(f);
 #pragma unroll
-      for (int k = 0; k < N; ++k) f[j][k] *= w ? r * c[k] : r;
-      if (b) {
-        bv[j].get(c);
+      for (int k = 0; k < N; ++k) f[k] = (f[k] - mu) * r;
+      if (w) {
+        v.load(w, i);
+        v.get(c);
 #pragma unroll
-        for (int k = 0; k < N; ++k) f[j][k] += c[k];
+        for (int k = 0; k < N; ++k) f[k] *= c[k];
       }
-      Row16<E>::store(y, t * nv + i, f[j]);
+      if (b) {
+        v.load(b, i);
+        v.get(c);
+#pragma unroll
+        for (int k = 0; k < N; ++k) f[k] += c[k];
+      }
+      Row16<E>::store(y, t * nv + i, f);
     }
     if (i0 == 0) {
       if (mean) mean[t] = mu;
       if (rstd) rstd[t] = r;
     }
   }
+  ring.drain();
 }
 
 template <typename E, typename D, int VPT>
 __global__ void __launch_bounds__(kBwdThreads)
-    norm_bwd_kernel(int64_t T, int H, int G, int rms, const E* __restrict__ x, const E* __restrict__ w,
+    norm_bwd_kernel(int64_t T, int H, int G, int slots, int rms, const E* __restrict__ x, const E* __restrict__ w,
                     const D* __restrict__ dy, const float* __restrict__ mean, const float* __restrict__ rstd,
-                    E* __restrict__ dx, float* __restrict__ part) {
+                    E* __restrict__ dx, float* __restrict__ part, int32_t* status, uint64_t limit_ns) {
   constexpr int N = Row16<E>::N;
-  __shared__ float sh[kMaxGroups][128];
-  __shared__ float col[2][4096];   // used when the CTA has several groups (H <= 4096)
+  __shared__ float sh[kMaxGroups][64];
+  __shared__ uint64_t full[kMaxGroups][kMaxSlots];
+  __shared__ int s_abort;
+  extern __shared__ __align__(16) char ring_mem[];
   grid_dep_launch();
-  grid_dep_wait();
   const int nv = H / N, groups = static_cast<int>(blockDim.x) / G;
   const int g = static_cast<int>(threadIdx.x) / G, i0 = static_cast<int>(threadIdx.x) % G;
+  const uint32_t x_bytes = static_cast<uint32_t>(H) * sizeof(E), d_bytes = static_cast<uint32_t>(H) * sizeof(D);
+  if (threadIdx.x == 0) s_abort = 0;
+  RowRing ring = make_ring(full, ring_mem, g, slots, x_bytes + d_bytes, i0 == 0, WaitCtx{&s_abort, status, limit_ns});
+  __syncthreads();
+  grid_dep_wait();
   const float inv = 1.0f / static_cast<float>(H);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const int warp = i0 >> 5, lane = static_cast<int>(threadIdx.x & 31);
   int buf = 0;
-  Row16<E> wv[VPT], xv[VPT];
-  RowN<D, N> dv[VPT];
+  Row16<E> wv[VPT];
   float aw[VPT][N], ab[VPT][N];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -225,20 +303,24 @@ __global__ void __launch_bounds__(kBwdThreads)
     for (int k = 0; k < N; ++k) aw[j][k] = ab[j][k] = 0.0f;
   }
   int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
+  auto fill = [&](int slot, int64_t row) {
+    if (!ring.lead || row >= T || !ring.ok) return;
+    char* to = ring.buf + static_cast<size_t>(slot) * ring.slot_bytes;
+    mbar_arrive_expect_tx(&ring.full[slot], ring.slot_bytes);
+    bulk_load(to, x + row * H, x_bytes, &ring.full[slot]);
+    bulk_load(to + x_bytes, dy + row * H, d_bytes, &ring.full[slot]);
+    ++ring.issued;
+  };
+  for (int i = 0; i < slots; ++i) fill(i, t + i * step);
   float mu = 0.0f, r = 0.0f;
-  auto fetch = [&](int64_t row) {
+  auto stats = [&](int64_t row) {   // fetched a row ahead
     if (row >= T) return;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (i0 + j * G < nv) {
-        xv[j].load(x, row * nv + i0 + j * G);
-        dv[j].load(dy, row * nv + i0 + j * G);
-      }
     mu = rms ? 0.0f : mean[row];
     r = rstd[row];
   };
-  fetch(t);
+  stats(t);
   for (; t < T; t += step) {
+    const char* row = ring.wait();
     float xh[VPT][N], gr[VPT][N];
     float sg = 0.0f, sx = 0.0f;
     const float rt = r;
@@ -246,8 +328,12 @@ __global__ void __launch_bounds__(kBwdThreads)
     for (int j = 0; j < VPT; ++j) {
       if (i0 + j * G >= nv) continue;
       float c[N];
-      xv[j].get(xh[j]);
-      dv[j].get(gr[j]);
+      Row16<E> xv;
+      RowN<D, N> dv;
+      xv.load(reinterpret_cast<const E*>(row), i0 + j * G);
+      dv.load(reinterpret_cast<const D*>(row + x_bytes), i0 + j * G);
+      xv.get(xh[j]);
+      dv.get(gr[j]);
       if (w) wv[j].get(c);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
@@ -259,28 +345,30 @@ __global__ void __launch_bounds__(kBwdThreads)
         sx = fmaf(gr[j][k], xh[j][k], sx);
       }
     }
-    fetch(t + step);
-    if (!dx) continue;
-    // both sums with one barrier
+    stats(t + step);
+    // both sums with one barrier, after which the group has also read the slot
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       sg += __shfl_xor_sync(0xffffffffu, sg, o);
       sx += __shfl_xor_sync(0xffffffffu, sx, o);
     }
     if (G > 32) {
-      float* s = sh[g] + 64 * buf;
+      float* s = sh[g] + 32 * buf;
       buf ^= 1;
       if (lane == 0) {
         s[2 * warp] = sg;
         s[2 * warp + 1] = sx;
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + g), "r"(G) : "memory");
+      group_sync(1 + g, G);
       sg = sx = 0.0f;
       for (int i = 0; i < (G >> 5); ++i) {
         sg += s[2 * i];
         sx += s[2 * i + 1];
       }
     }
+    fill(ring.slot, t + slots * step);
+    ring.next();
+    if (!dx) continue;
     const float mg = rms ? 0.0f : sg * inv, mx = sx * inv;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -290,9 +378,13 @@ __global__ void __launch_bounds__(kBwdThreads)
       Row16<E>::store(dx, t * nv + i0 + j * G, gr[j]);
     }
   }
+  ring.drain();
   if (!part) return;
-  // The groups' column sums are added in group order. Element k of vector i is kept
-  // at k * nv + i, so that a warp's accesses fall into different banks.
+  // The groups' column sums are added in group order, through the ring's memory
+  // once every group is done with it. Element k of vector i is kept at k * nv + i,
+  // so that a warp's accesses fall into different banks.
+  if (groups > 1) __syncthreads();
+  float* col = reinterpret_cast<float*>(ring_mem);
   float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * H;
   for (int turn = 0; turn < groups; ++turn) {
     if (turn == g) {
@@ -303,12 +395,12 @@ __global__ void __launch_bounds__(kBwdThreads)
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           if (turn > 0) {
-            aw[j][k] = col[0][k * nv + i] + aw[j][k];
-            ab[j][k] = col[1][k * nv + i] + ab[j][k];
+            aw[j][k] = col[k * nv + i] + aw[j][k];
+            ab[j][k] = col[H + k * nv + i] + ab[j][k];
           }
           if (turn < groups - 1) {
-            col[0][k * nv + i] = aw[j][k];
-            col[1][k * nv + i] = ab[j][k];
+            col[k * nv + i] = aw[j][k];
+            col[H + k * nv + i] = ab[j][k];
           }
         }
         if (turn == groups - 1) {
@@ -422,13 +514,14 @@ __global__ void __launch_bounds__(kBwdThreads)
   }
 }
 
+constexpr int kColThreads = 256;
 template <typename E, typename D>
-__global__ void __launch_bounds__(kFwdThreads)
+__global__ void __launch_bounds__(kColThreads)
     norm_wide_dw_kernel(int64_t T, int H, int rms, const E* __restrict__ x, const D* __restrict__ dy,
                         const float* __restrict__ mean, const float* __restrict__ rstd, float* __restrict__ part) {
   grid_dep_launch();
   grid_dep_wait();
-  const int i = blockIdx.x * kFwdThreads + threadIdx.x;
+  const int i = blockIdx.x * kColThreads + threadIdx.x;
   if (i >= H) return;
   float a = 0.0f, b = 0.0f;
   for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
@@ -448,71 +541,108 @@ int group_size(int64_t nv, int most, int cap) {
   return G;
 }
 
-struct BwdShape {
+// A launch: groups of G threads, as many to a CTA as keep every SM in work, and
+// the slots of each group's ring.
+struct Shape {
   bool fused;
-  int G, groups, vpt, parts;
+  int G, groups, slots, ctas;
+  size_t smem;
 };
-BwdShape bwd_shape(const vce_problem& p) {
-  BwdShape s{};
+Shape shape(const vce_problem& p, int most, int cap_threads, int64_t slot_bytes, int64_t min_smem) {
+  Shape s{};
   const int64_t nv = p.H / (p.dtype == VCE_BF16 ? 8 : 4);
-  const int sms = current_device_info().num_sms;
-  s.fused = nv <= 2 * kBwdThreads;
-  s.G = group_size(nv, 2, kBwdThreads);
-  s.groups = kBwdThreads / s.G;
-  s.vpt = nv <= s.G ? 1 : 2;
-  const int64_t want = s.fused ? ceil_div(p.T, s.groups) : p.T;
-  s.parts = static_cast<int>(want < sms ? want : sms);
+  const int64_t sms = current_device_info().num_sms;
+  s.fused = nv <= static_cast<int64_t>(most) * cap_threads;
+  s.G = group_size(nv, most, cap_threads);
+  int64_t groups = cap_threads / s.G;
+  if (groups > kNamedBarriers && s.G > 32) groups = kNamedBarriers;
+  const int64_t want = ceil_div(p.T, sms);
+  if (groups > want) groups = want;
+  if (groups * slot_bytes > kRingBytes) groups = kRingBytes / slot_bytes;
+  if (groups < 1) {
+    s.fused = false;
+    groups = 1;
+  }
+  s.groups = static_cast<int>(groups);
+  const int64_t slots = kRingBytes / (groups * slot_bytes);
+  s.slots = static_cast<int>(slots < 1 ? 1 : slots > kMaxSlots ? kMaxSlots : slots);
+  const int64_t rows = s.fused ? ceil_div(p.T, groups) : p.T;
+  s.ctas = static_cast<int>(rows < sms ? rows : sms);
+  s.smem = static_cast<size_t>(groups) * s.slots * slot_bytes;
+  if (s.smem < static_cast<size_t>(min_smem)) s.smem = static_cast<size_t>(min_smem);
   return s;
 }
+Shape fwd_shape(const vce_problem& p) { return shape(p, 4, kFwdThreads, p.H * (p.dtype == VCE_BF16 ? 2 : 4), 0); }
+Shape bwd_shape(const vce_problem& p) {
+  const int64_t row = p.H * ((p.dtype == VCE_BF16 ? 2 : 4) + ((p.flags & VCE_FLAG_DH_BF16) ? 2 : 4));
+  return shape(p, 2, kBwdThreads, row, 2 * p.H * static_cast<int64_t>(sizeof(float)));
+}
 
-template <typename E>
-cudaError_t fwd_typed(const vce_problem& p, bool rms, const void* x, const void* w, const void* b, float eps, void* y,
-                      float* mean, float* rstd, cudaStream_t st) {
-  const int64_t nv = p.H / Row16<E>::N;
-  if (nv > 4096) {
-    const cudaError_t e = launch_dependent(norm_wide_fwd_kernel<E>, dim3(static_cast<unsigned>(p.T)), dim3(kBwdThreads),
-                                           0, st, static_cast<int>(p.H), rms ? 1 : 0, static_cast<const E*>(x),
-                                           static_cast<const E*>(w), static_cast<const E*>(b), eps,
-                                           static_cast<E*>(y), mean, rstd);
-    note_launch(VCE_K_NORM_FWD, st);
-    return e;
+// Raises the kernel's shared-memory limit once per device, then launches it.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_ring(void (*kern)(KArgs...), std::atomic<uint64_t>& configured, const Shape& s, cudaStream_t st,
+                        Args... args) {
+  if (device_pending(configured)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kRingBytes));
+    if (e != cudaSuccess) return e;
+    mark_device_done(configured);
   }
-  const int G = group_size(nv, 2, 1024);
-  const int threads = G > kFwdThreads ? G : kFwdThreads, groups = threads / G;
-  const int64_t want = ceil_div(p.T, groups);
-  const int64_t cap = static_cast<int64_t>(current_device_info().num_sms) * (1024 / threads);   // resident at 64 registers
-  const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
-  const int64_t vpt = ceil_div(nv, G);
-  auto go = [&](auto kern) {
-    return launch_dependent(kern, grid, dim3(threads), 0, st, p.T, static_cast<int>(p.H), G, rms ? 1 : 0,
-                            static_cast<const E*>(x), static_cast<const E*>(w), static_cast<const E*>(b), eps,
-                            static_cast<E*>(y), mean, rstd);
-  };
-  const cudaError_t e = vpt <= 1   ? go(norm_fwd_kernel<E, 1>)
-                        : vpt <= 2 ? go(norm_fwd_kernel<E, 2>)
-                                   : go(norm_fwd_kernel<E, 4>);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(s.ctas)), dim3(static_cast<unsigned>(s.groups * s.G)),
+                          s.smem, st, args...);
+}
+
+template <typename E, int VPT>
+cudaError_t fwd_vpt(const vce_problem& p, const Shape& s, bool rms, const E* x, const E* w, const E* b, float eps, E* y,
+                    float* mean, float* rstd, int32_t* status, cudaStream_t st) {
+  static std::atomic<uint64_t> configured{0};
+  return launch_ring(norm_fwd_kernel<E, VPT>, configured, s, st, p.T, static_cast<int>(p.H), s.G, s.slots, rms ? 1 : 0,
+                     x, w, b, eps, y, mean, rstd, status, wait_limit_ns());
+}
+template <typename E>
+cudaError_t fwd_typed(const vce_problem& p, bool rms, const void* x_, const void* w_, const void* b_, float eps,
+                      void* y_, float* mean, float* rstd, int32_t* status, cudaStream_t st) {
+  const E* x = static_cast<const E*>(x_);
+  const E* w = static_cast<const E*>(w_);
+  const E* b = static_cast<const E*>(b_);
+  E* y = static_cast<E*>(y_);
+  const Shape s = fwd_shape(p);
+  const int64_t nv = p.H / Row16<E>::N, vpt = ceil_div(nv, s.G);
+  cudaError_t e;
+  if (!s.fused)
+    e = launch_dependent(norm_wide_fwd_kernel<E>, dim3(static_cast<unsigned>(p.T)), dim3(kBwdThreads), 0, st,
+                         static_cast<int>(p.H), rms ? 1 : 0, x, w, b, eps, y, mean, rstd);
+  else
+    e = vpt <= 1   ? fwd_vpt<E, 1>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st)
+        : vpt <= 2 ? fwd_vpt<E, 2>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st)
+                   : fwd_vpt<E, 4>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st);
   note_launch(VCE_K_NORM_FWD, st);
   return e;
 }
 
+template <typename E, typename D, int VPT>
+cudaError_t bwd_vpt(const vce_problem& p, const Shape& s, bool rms, const E* x, const E* w, const D* dy,
+                    const float* mean, const float* rstd, E* dx, float* part, int32_t* status, cudaStream_t st) {
+  static std::atomic<uint64_t> configured{0};
+  return launch_ring(norm_bwd_kernel<E, D, VPT>, configured, s, st, p.T, static_cast<int>(p.H), s.G, s.slots,
+                     rms ? 1 : 0, x, w, dy, mean, rstd, dx, part, status, wait_limit_ns());
+}
 template <typename E, typename D>
 cudaError_t bwd_typed(const vce_problem& p, bool rms, const void* x_, const void* w_, const void* dy_,
                       const float* mean, const float* rstd, void* dx_, float* dw, float* db, bool accumulate,
-                      float* part, cudaStream_t st) {
+                      float* part, int32_t* status, cudaStream_t st) {
   const E* x = static_cast<const E*>(x_);
   const E* w = static_cast<const E*>(w_);
   const D* dy = static_cast<const D*>(dy_);
   E* dx = static_cast<E*>(dx_);
-  const BwdShape s = bwd_shape(p);
+  const Shape s = bwd_shape(p);
   const int H = static_cast<int>(p.H);
   const bool sums = dw || db;
   cudaError_t e = cudaSuccess;
   if (s.fused) {
-    auto go = [&](auto kern) {
-      return launch_dependent(kern, dim3(static_cast<unsigned>(s.parts)), dim3(kBwdThreads), 0, st, p.T, H, s.G,
-                              rms ? 1 : 0, x, w, dy, mean, rstd, dx, sums ? part : nullptr);
-    };
-    e = s.vpt == 1 ? go(norm_bwd_kernel<E, D, 1>) : go(norm_bwd_kernel<E, D, 2>);
+    const bool one = p.H / Row16<E>::N <= s.G;
+    e = one ? bwd_vpt<E, D, 1>(p, s, rms, x, w, dy, mean, rstd, dx, sums ? part : nullptr, status, st)
+            : bwd_vpt<E, D, 2>(p, s, rms, x, w, dy, mean, rstd, dx, sums ? part : nullptr, status, st);
     note_launch(VCE_K_NORM_BWD, st);
   } else {
     if (dx) {
@@ -522,13 +652,13 @@ cudaError_t bwd_typed(const vce_problem& p, bool rms, const void* x_, const void
     }
     if (e == cudaSuccess && sums) {
       e = launch_dependent(norm_wide_dw_kernel<E, D>,
-                           dim3(static_cast<unsigned>(ceil_div(H, kFwdThreads)), static_cast<unsigned>(s.parts)),
-                           dim3(kFwdThreads), 0, st, p.T, H, rms ? 1 : 0, x, dy, mean, rstd, part);
+                           dim3(static_cast<unsigned>(ceil_div(H, kColThreads)), static_cast<unsigned>(s.ctas)),
+                           dim3(kColThreads), 0, st, p.T, H, rms ? 1 : 0, x, dy, mean, rstd, part);
       note_launch(VCE_K_NORM_BWD, st);
     }
   }
   if (e != cudaSuccess || !sums) return e;
-  e = launch_dependent(norm_sum_kernel, dim3(static_cast<unsigned>(ceil_div(H, 32))), dim3(512), 0, st, H, s.parts,
+  e = launch_dependent(norm_sum_kernel, dim3(static_cast<unsigned>(ceil_div(H, 32))), dim3(512), 0, st, H, s.ctas,
                        accumulate ? 1 : 0, static_cast<const float*>(part), dw, db);
   note_launch(VCE_K_NORM_SUM, st);
   return e;
@@ -537,20 +667,21 @@ cudaError_t bwd_typed(const vce_problem& p, bool rms, const void* x_, const void
 }  // namespace
 
 size_t norm_ws_bytes(const vce_problem& p) {
-  return align_up(static_cast<size_t>(bwd_shape(p).parts) * 2 * static_cast<size_t>(p.H) * sizeof(float), kWsAlign);
+  return align_up(static_cast<size_t>(bwd_shape(p).ctas) * 2 * static_cast<size_t>(p.H) * sizeof(float), kWsAlign);
 }
 
 cudaError_t launch_norm_fwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* b, float eps,
-                            void* y, float* mean, float* rstd, cudaStream_t st) {
-  return p.dtype == VCE_BF16 ? fwd_typed<__nv_bfloat16>(p, rms, x, w, b, eps, y, mean, rstd, st)
-                             : fwd_typed<float>(p, rms, x, w, b, eps, y, mean, rstd, st);
+                            void* y, float* mean, float* rstd, int32_t* status, cudaStream_t st) {
+  return p.dtype == VCE_BF16 ? fwd_typed<__nv_bfloat16>(p, rms, x, w, b, eps, y, mean, rstd, status, st)
+                             : fwd_typed<float>(p, rms, x, w, b, eps, y, mean, rstd, status, st);
 }
 
-cudaError_t launch_norm_bwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* dy, bool dy_bf16,
+cudaError_t launch_norm_bwd(const vce_problem& p, bool rms, const void* x, const void* w, const void* dy,
                             const float* mean, const float* rstd, void* dx, float* dw, float* db, bool accumulate,
-                            void* ws, cudaStream_t st) {
+                            void* ws, int32_t* status, cudaStream_t st) {
   float* part = static_cast<float*>(ws);
-  auto go = [&](auto f) { return f(p, rms, x, w, dy, mean, rstd, dx, dw, db, accumulate, part, st); };
+  const bool dy_bf16 = (p.flags & VCE_FLAG_DH_BF16) != 0;
+  auto go = [&](auto f) { return f(p, rms, x, w, dy, mean, rstd, dx, dw, db, accumulate, part, status, st); };
   if (p.dtype == VCE_BF16)
     return dy_bf16 ? go(bwd_typed<__nv_bfloat16, __nv_bfloat16>) : go(bwd_typed<__nv_bfloat16, float>);
   return dy_bf16 ? go(bwd_typed<float, __nv_bfloat16>) : go(bwd_typed<float, float>);

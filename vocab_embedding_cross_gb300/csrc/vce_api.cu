@@ -805,7 +805,7 @@ vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, c
 }
 
 vce_status vce_norm_fwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* bias,
-                        float eps, void* y, float* mean, float* rstd, void* stream) {
+                        float eps, void* y, float* mean, float* rstd, int32_t* dev_status, void* stream) {
   vce_status s = check_problem(p);
   if (s != VCE_OK) return s;
   if (kind != VCE_NORM_LAYER && kind != VCE_NORM_RMS) return VCE_ERR_ARG;
@@ -815,13 +815,13 @@ vce_status vce_norm_fwd(const vce_problem* p, int32_t kind, const void* x, const
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(weight, 16) || !aligned(bias, 16) || !aligned(mean, 4) ||
       !aligned(rstd, 4))
     return VCE_ERR_UNSUPPORTED;
-  return cuda_status(launch_norm_fwd(*p, kind == VCE_NORM_RMS, x, weight, bias, eps, y, mean, rstd,
+  return cuda_status(launch_norm_fwd(*p, kind == VCE_NORM_RMS, x, weight, bias, eps, y, mean, rstd, dev_status,
                                      static_cast<cudaStream_t>(stream)));
 }
 
 vce_status vce_norm_bwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* dy,
                         const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,
-                        int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+                        int32_t accumulate, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
   vce_status s = check_problem(p);
   if (s != VCE_OK) return s;
   if (kind != VCE_NORM_LAYER && kind != VCE_NORM_RMS) return VCE_ERR_ARG;
@@ -839,8 +839,8 @@ vce_status vce_norm_bwd(const vce_problem* p, int32_t kind, const void* x, const
       !aligned(rstd, 4) || !aligned(dweight, 16) || !aligned(dbias, 16))
     return VCE_ERR_UNSUPPORTED;
   if (!ws || !aligned(ws, kWsAlign) || ws_bytes < norm_ws_bytes(*p)) return VCE_ERR_WORKSPACE;
-  return cuda_status(launch_norm_bwd(*p, kind == VCE_NORM_RMS, x, weight, dy, (p->flags & VCE_FLAG_DH_BF16) != 0, mean,
-                                     rstd, dx, dweight, dbias, accumulate != 0, ws, st));
+  return cuda_status(launch_norm_bwd(*p, kind == VCE_NORM_RMS, x, weight, dy, mean, rstd, dx, dweight, dbias,
+                                     accumulate != 0, ws, dev_status, st));
 }
 
 vce_status vce_ngram_hash(const int64_t* ids, int64_t T, int32_t n, int64_t V, int64_t M, int64_t seq_len,
