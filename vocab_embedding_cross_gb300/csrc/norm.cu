@@ -156,7 +156,7 @@ struct RowRing {
   bool ok, lead;
   WaitCtx wc;
   __device__ __forceinline__ char* wait() {
-    ok = ok && mbar_wait(&full[slot], phase, wc);
+    ok = ok && wait_late(&full[slot], phase, wc);
     return buf + static_cast<size_t>(slot) * slot_bytes;
   }
   __device__ __forceinline__ void next() {
@@ -185,10 +185,12 @@ __device__ __forceinline__ RowRing make_ring(uint64_t (*full)[kMaxSlots], char* 
   return RowRing{full[g], smem + static_cast<size_t>(g) * slots * slot_bytes, slot_bytes, slots, 0, 0, 0, true, lead, wc};
 }
 
-// VPT vectors of 16 bytes a thread (up to four), kept as they were stored.
-template <typename E, int VPT>
+// VPT vectors of 16 bytes a thread (up to four). The kernel is near the limit of
+// what an SM issues, so what is fixed for a launch is fixed in the code: RMS, and
+// FULL, every thread having exactly VPT vectors (H = 8 VPT G in bf16).
+template <typename E, int VPT, bool RMS, bool FULL>
 __global__ void __launch_bounds__(kFwdThreads)
-    norm_fwd_kernel(int64_t T, int H, int G, int slots, int rms, const E* __restrict__ x, const E* __restrict__ w,
+    norm_fwd_kernel(int64_t T, int H, int G, int slots, const E* __restrict__ x, const E* __restrict__ w,
                     const E* __restrict__ b, float eps, E* __restrict__ y, float* __restrict__ mean,
                     float* __restrict__ rstd, int32_t* status, uint64_t limit_ns) {
   constexpr int N = Row16<E>::N;
@@ -216,53 +218,67 @@ __global__ void __launch_bounds__(kFwdThreads)
   };
   for (int i = 0; i < slots; ++i) fill(i, t + i * step);
   for (; t < T; t += step) {
-    const uint4* row = reinterpret_cast<const uint4*>(ring.wait());
-    Row16<E> xv[VPT];
-    float s = 0.0f;
+    const E* row = reinterpret_cast<const E*>(ring.wait());
+    float f[VPT][N];
+    float s = 0.0f, q = 0.0f, mu = 0.0f;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (i0 + j * G < nv) {
-        xv[j].load(reinterpret_cast<const E*>(row), i0 + j * G);
-        float f[N];
-        xv[j].get(f);
+    for (int j = 0; j < VPT; ++j) {
+      if (FULL || i0 + j * G < nv) {
+        Row16<E> v;
+        v.load(row, i0 + j * G);
+        v.get(f[j]);
 #pragma unroll
-        for (int k = 0; k < N; ++k) s += f[k];
+        for (int k = 0; k < N; ++k) {
+          if (RMS)
+            q = fmaf(f[j][k], f[j][k], q);
+          else
+            s += f[j][k];
+        }
       }
-    const float mu = rms ? 0.0f : sum(s) * inv;
-    float q = 0.0f;
+    }
+    if (!RMS) {
+      mu = sum(s) * inv;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j)
-      if (i0 + j * G < nv) {
-        float f[N];
-        xv[j].get(f);
+      for (int j = 0; j < VPT; ++j)
+        if (FULL || i0 + j * G < nv) {
 #pragma unroll
-        for (int k = 0; k < N; ++k) q = fmaf(f[k] - mu, f[k] - mu, q);
-      }
-    const float r = 1.0f / sqrtf(sum(q) * inv + eps);   // the whole group has read the slot
-    fill(ring.slot, t + slots * step);
+          for (int k = 0; k < N; ++k) {
+            f[j][k] -= mu;
+            q = fmaf(f[j][k], f[j][k], q);
+          }
+        }
+    }
+    const float r = __frsqrt_rn(fmaf(sum(q), inv, eps));
+    if (RMS && G == 32) __syncwarp();
+    fill(ring.slot, t + slots * step);   // the whole group has read the slot
     ring.next();
+    E* out = y + t * H;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int i = i0 + j * G;
-      if (i >= nv) continue;
-      float f[N], c[N];
+      if (!FULL && i >= nv) continue;
+      float c[N], d[N];
       Row16<E> v;
-      xv[j].get(f);
 #pragma unroll
-      for (int k = 0; k < N; ++k) f[k] = (f[k] - mu) * r;
+      for (int k = 0; k < N; ++k) f[j][k] *= r;
       if (w) {
         v.load(w, i);
         v.get(c);
-#pragma unroll
-        for (int k = 0; k < N; ++k) f[k] *= c[k];
       }
       if (b) {
         v.load(b, i);
-        v.get(c);
-#pragma unroll
-        for (int k = 0; k < N; ++k) f[k] += c[k];
+        v.get(d);
       }
-      Row16<E>::store(y, t * nv + i, f);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        if (w && b)
+          f[j][k] = fmaf(f[j][k], c[k], d[k]);
+        else if (w)
+          f[j][k] *= c[k];
+        else if (b)
+          f[j][k] += d[k];
+      }
+      Row16<E>::store(out, i, f[j]);
     }
     if (i0 == 0) {
       if (mean) mean[t] = mu;
@@ -592,12 +608,20 @@ cudaError_t launch_ring(void (*kern)(KArgs...), std::atomic<uint64_t>& configure
                           s.smem, st, args...);
 }
 
+template <typename E, int VPT, bool RMS, bool FULL>
+cudaError_t fwd_as(const vce_problem& p, const Shape& s, const E* x, const E* w, const E* b, float eps, E* y,
+                   float* mean, float* rstd, int32_t* status, cudaStream_t st) {
+  static std::atomic<uint64_t> configured{0};
+  return launch_ring(norm_fwd_kernel<E, VPT, RMS, FULL>, configured, s, st, p.T, static_cast<int>(p.H), s.G, s.slots, x,
+                     w, b, eps, y, mean, rstd, status, wait_limit_ns());
+}
 template <typename E, int VPT>
 cudaError_t fwd_vpt(const vce_problem& p, const Shape& s, bool rms, const E* x, const E* w, const E* b, float eps, E* y,
                     float* mean, float* rstd, int32_t* status, cudaStream_t st) {
-  static std::atomic<uint64_t> configured{0};
-  return launch_ring(norm_fwd_kernel<E, VPT>, configured, s, st, p.T, static_cast<int>(p.H), s.G, s.slots, rms ? 1 : 0,
-                     x, w, b, eps, y, mean, rstd, status, wait_limit_ns());
+  const bool full = p.H == static_cast<int64_t>(VPT) * s.G * Row16<E>::N;
+  auto go = [&](auto f) { return f(p, s, x, w, b, eps, y, mean, rstd, status, st); };
+  return rms ? (full ? go(fwd_as<E, VPT, true, true>) : go(fwd_as<E, VPT, true, false>))
+             : (full ? go(fwd_as<E, VPT, false, true>) : go(fwd_as<E, VPT, false, false>));
 }
 template <typename E>
 cudaError_t fwd_typed(const vce_problem& p, bool rms, const void* x_, const void* w_, const void* b_, float eps,

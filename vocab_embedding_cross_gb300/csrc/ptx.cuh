@@ -118,6 +118,41 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, w);
 }
 
+// A try that the hardware may suspend for up to 20 us before it says no.
+__device__ __forceinline__ bool try_wait_long(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+
+// mbar_wait for a pipeline that often has to wait: the clock is read only after
+// 64 unsuccessful tries, each of which the hardware suspends for a while.
+static __device__ __noinline__ bool wait_later(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (try_wait_long(bar, parity)) return true;
+    if ((it & 63u) == 0u) {
+      if (*w.abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > w.limit_ns) {
+        *w.abort = 1;
+        record_status(w.status, 5);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool wait_late(uint64_t* bar, uint32_t parity, const WaitCtx& w) {
+  return mbar_try_wait(bar, parity) || wait_later(bar, parity, w);
+}
+
 // ---------------------------------------------------------------------------
 // TMA (cp.async.bulk.tensor), 2-D tiles. x is the inner (contiguous)
 // coordinate in elements, y the row. Loads complete on an mbarrier.
