@@ -128,7 +128,7 @@ struct GroupSum {
   }
 };
 
-constexpr int kFwdThreads = 1024;
+constexpr int kFwdThreads = 512;
 constexpr int kBwdThreads = 512;
 constexpr int kMaxGroups = 32;
 constexpr int kMaxSlots = 4;
@@ -185,9 +185,11 @@ __device__ __forceinline__ RowRing make_ring(uint64_t (*full)[kMaxSlots], char* 
   return RowRing{full[g], smem + static_cast<size_t>(g) * slots * slot_bytes, slot_bytes, slots, 0, 0, 0, true, lead, wc};
 }
 
-// VPT vectors of 16 bytes a thread (up to four). The kernel is near the limit of
-// what an SM issues, so what is fixed for a launch is fixed in the code: RMS, and
-// FULL, every thread having exactly VPT vectors (H = 8 VPT G in bf16).
+// VPT vectors of 16 bytes a thread (up to eight: a warp alone takes a row of 2048
+// bf16, and no barrier stands between its statistics and its output). The kernel
+// is nearer to what an SM issues than to what memory delivers, so what is fixed
+// for a launch is fixed in the code: RMS, and FULL, every thread having exactly
+// VPT vectors. The weights are read from shared memory.
 template <typename E, int VPT, bool RMS, bool FULL>
 __global__ void __launch_bounds__(kFwdThreads)
     norm_fwd_kernel(int64_t T, int H, int G, int slots, const E* __restrict__ x, const E* __restrict__ w,
@@ -197,17 +199,16 @@ __global__ void __launch_bounds__(kFwdThreads)
   __shared__ float sh[kMaxGroups][64];
   __shared__ uint64_t full[kMaxGroups][kMaxSlots];
   __shared__ int s_abort;
-  extern __shared__ __align__(16) char ring_mem[];
+  extern __shared__ __align__(16) char ring_mem[];   // weight row, bias row, rings
   grid_dep_launch();
   const int nv = H / N, groups = static_cast<int>(blockDim.x) / G;
   const int g = static_cast<int>(threadIdx.x) / G, i0 = static_cast<int>(threadIdx.x) % G;
+  const uint32_t row_bytes = static_cast<uint32_t>(nv) * 16u;
   if (threadIdx.x == 0) s_abort = 0;
-  RowRing ring = make_ring(full, ring_mem, g, slots, static_cast<uint32_t>(nv) * 16u, i0 == 0,
+  RowRing ring = make_ring(full, ring_mem + 2 * row_bytes, g, slots, row_bytes, i0 == 0,
                            WaitCtx{&s_abort, status, limit_ns});
   __syncthreads();
   grid_dep_wait();
-  GroupSum sum{sh[g], G, 1 + g, 0};
-  const float inv = 1.0f / static_cast<float>(H);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
   auto fill = [&](int slot, int64_t row) {
@@ -217,10 +218,18 @@ __global__ void __launch_bounds__(kFwdThreads)
     ++ring.issued;
   };
   for (int i = 0; i < slots; ++i) fill(i, t + i * step);
+  uint4* sw = reinterpret_cast<uint4*>(ring_mem);
+  for (int i = threadIdx.x; i < nv; i += blockDim.x) {
+    if (w) sw[i] = reinterpret_cast<const uint4*>(w)[i];
+    if (b) sw[nv + i] = reinterpret_cast<const uint4*>(b)[i];
+  }
+  __syncthreads();
+  GroupSum sum{sh[g], G, 1 + g, 0};
+  const float inv = 1.0f / static_cast<float>(H);
   for (; t < T; t += step) {
     const E* row = reinterpret_cast<const E*>(ring.wait());
     float f[VPT][N];
-    float s = 0.0f, q = 0.0f, mu = 0.0f;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, mu = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (FULL || i0 + j * G < nv) {
@@ -228,28 +237,24 @@ __global__ void __launch_bounds__(kFwdThreads)
         v.load(row, i0 + j * G);
         v.get(f[j]);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          if (RMS)
-            q = fmaf(f[j][k], f[j][k], q);
-          else
-            s += f[j][k];
-        }
+        for (int k = 0; k < N; ++k) acc[k & 3] = RMS ? fmaf(f[j][k], f[j][k], acc[k & 3]) : acc[k & 3] + f[j][k];
       }
     }
     if (!RMS) {
-      mu = sum(s) * inv;
+      mu = sum((acc[0] + acc[1]) + (acc[2] + acc[3])) * inv;
+      acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
         if (FULL || i0 + j * G < nv) {
 #pragma unroll
           for (int k = 0; k < N; ++k) {
             f[j][k] -= mu;
-            q = fmaf(f[j][k], f[j][k], q);
+            acc[k & 3] = fmaf(f[j][k], f[j][k], acc[k & 3]);
           }
         }
     }
-    const float r = __frsqrt_rn(fmaf(sum(q), inv, eps));
-    if (RMS && G == 32) __syncwarp();
+    const float r = __frsqrt_rn(fmaf(sum((acc[0] + acc[1]) + (acc[2] + acc[3])), inv, eps));
+    __syncwarp();
     fill(ring.slot, t + slots * step);   // the whole group has read the slot
     ring.next();
     E* out = y + t * H;
@@ -262,11 +267,11 @@ __global__ void __launch_bounds__(kFwdThreads)
 #pragma unroll
       for (int k = 0; k < N; ++k) f[j][k] *= r;
       if (w) {
-        v.load(w, i);
+        v.load(reinterpret_cast<const E*>(sw), i);
         v.get(c);
       }
       if (b) {
-        v.load(b, i);
+        v.load(reinterpret_cast<const E*>(sw + nv), i);
         v.get(d);
       }
 #pragma unroll
@@ -564,7 +569,8 @@ struct Shape {
   int G, groups, slots, ctas;
   size_t smem;
 };
-Shape shape(const vce_problem& p, int most, int cap_threads, int64_t slot_bytes, int64_t min_smem) {
+Shape shape(const vce_problem& p, int most, int cap_threads, int64_t slot_bytes, int64_t fixed_bytes,
+            int64_t min_smem) {
   Shape s{};
   const int64_t nv = p.H / (p.dtype == VCE_BF16 ? 8 : 4);
   const int64_t sms = current_device_info().num_sms;
@@ -574,24 +580,28 @@ Shape shape(const vce_problem& p, int most, int cap_threads, int64_t slot_bytes,
   if (groups > kNamedBarriers && s.G > 32) groups = kNamedBarriers;
   const int64_t want = ceil_div(p.T, sms);
   if (groups > want) groups = want;
-  if (groups * slot_bytes > kRingBytes) groups = kRingBytes / slot_bytes;
+  const int64_t room = static_cast<int64_t>(kRingBytes) - fixed_bytes;
+  if (groups * slot_bytes > room) groups = room / slot_bytes;
   if (groups < 1) {
     s.fused = false;
     groups = 1;
   }
   s.groups = static_cast<int>(groups);
-  const int64_t slots = kRingBytes / (groups * slot_bytes);
+  const int64_t slots = room / (groups * slot_bytes);
   s.slots = static_cast<int>(slots < 1 ? 1 : slots > kMaxSlots ? kMaxSlots : slots);
   const int64_t rows = s.fused ? ceil_div(p.T, groups) : p.T;
   s.ctas = static_cast<int>(rows < sms ? rows : sms);
-  s.smem = static_cast<size_t>(groups) * s.slots * slot_bytes;
+  s.smem = static_cast<size_t>(groups * s.slots * slot_bytes + fixed_bytes);
   if (s.smem < static_cast<size_t>(min_smem)) s.smem = static_cast<size_t>(min_smem);
   return s;
 }
-Shape fwd_shape(const vce_problem& p) { return shape(p, 4, kFwdThreads, p.H * (p.dtype == VCE_BF16 ? 2 : 4), 0); }
+Shape fwd_shape(const vce_problem& p) {
+  const int64_t row = p.H * (p.dtype == VCE_BF16 ? 2 : 4);
+  return shape(p, 8, kFwdThreads, row, 2 * row, 0);
+}
 Shape bwd_shape(const vce_problem& p) {
   const int64_t row = p.H * ((p.dtype == VCE_BF16 ? 2 : 4) + ((p.flags & VCE_FLAG_DH_BF16) ? 2 : 4));
-  return shape(p, 2, kBwdThreads, row, 2 * p.H * static_cast<int64_t>(sizeof(float)));
+  return shape(p, 2, kBwdThreads, row, 0, 2 * p.H * static_cast<int64_t>(sizeof(float)));
 }
 
 // Raises the kernel's shared-memory limit once per device, then launches it.
@@ -639,7 +649,8 @@ cudaError_t fwd_typed(const vce_problem& p, bool rms, const void* x_, const void
   else
     e = vpt <= 1   ? fwd_vpt<E, 1>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st)
         : vpt <= 2 ? fwd_vpt<E, 2>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st)
-                   : fwd_vpt<E, 4>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st);
+        : vpt <= 4 ? fwd_vpt<E, 4>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st)
+                   : fwd_vpt<E, 8>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st);
   note_launch(VCE_K_NORM_FWD, st);
   return e;
 }
