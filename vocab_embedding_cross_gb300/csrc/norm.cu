@@ -129,7 +129,8 @@ struct GroupSum {
 };
 
 constexpr int kFwdThreads = 512;
-constexpr int kBwdThreads = 512;
+constexpr int kBwdThreads = 256;
+constexpr int kWideThreads = 512;
 constexpr int kMaxGroups = 32;
 constexpr int kMaxSlots = 4;
 constexpr uint32_t kRingBytes = 200 * 1024;
@@ -293,9 +294,12 @@ __global__ void __launch_bounds__(kFwdThreads)
   ring.drain();
 }
 
-template <typename E, typename D, int VPT>
+// As the forward, with two sums a row, and the weight gradients of the thread's
+// VPT vectors in registers (64 of them at four vectors of bf16, so 256 threads an
+// SM; the ring keeps memory busy without more).
+template <typename E, typename D, int VPT, bool RMS, bool FULL>
 __global__ void __launch_bounds__(kBwdThreads)
-    norm_bwd_kernel(int64_t T, int H, int G, int slots, int rms, const E* __restrict__ x, const E* __restrict__ w,
+    norm_bwd_kernel(int64_t T, int H, int G, int slots, const E* __restrict__ x, const E* __restrict__ w,
                     const D* __restrict__ dy, const float* __restrict__ mean, const float* __restrict__ rstd,
                     E* __restrict__ dx, float* __restrict__ part, int32_t* status, uint64_t limit_ns) {
   constexpr int N = Row16<E>::N;
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   float aw[VPT][N], ab[VPT][N];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
-    if (w && i0 + j * G < nv) wv[j].load(w, i0 + j * G);
+    if (w && (FULL || i0 + j * G < nv)) wv[j].load(w, i0 + j * G);
 #pragma unroll
     for (int k = 0; k < N; ++k) aw[j][k] = ab[j][k] = 0.0f;
   }
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kBwdThreads)
   float mu = 0.0f, r = 0.0f;
   auto stats = [&](int64_t row) {   // fetched a row ahead
     if (row >= T) return;
-    mu = rms ? 0.0f : mean[row];
+    mu = RMS ? 0.0f : mean[row];
     r = rstd[row];
   };
   stats(t);
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kBwdThreads)
     const float rt = r;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if (i0 + j * G >= nv) continue;
+      if (!FULL && i0 + j * G >= nv) continue;
       float c[N];
       Row16<E> xv;
       RowN<D, N> dv;
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(kBwdThreads)
         aw[j][k] = fmaf(gr[j][k], xh[j][k], aw[j][k]);
         ab[j][k] += gr[j][k];
         if (w) gr[j][k] *= c[k];
-        sg += gr[j][k];
+        if (!RMS) sg += gr[j][k];
         sx = fmaf(gr[j][k], xh[j][k], sx);
       }
     }
@@ -370,7 +374,7 @@ __global__ void __launch_bounds__(kBwdThreads)
     // both sums with one barrier, after which the group has also read the slot
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+      if (!RMS) sg += __shfl_xor_sync(0xffffffffu, sg, o);
       sx += __shfl_xor_sync(0xffffffffu, sx, o);
     }
     if (G > 32) {
@@ -387,89 +391,112 @@ __global__ void __launch_bounds__(kBwdThreads)
         sx += s[2 * i + 1];
       }
     }
+    __syncwarp();
     fill(ring.slot, t + slots * step);
     ring.next();
     if (!dx) continue;
-    const float mg = rms ? 0.0f : sg * inv, mx = sx * inv;
+    E* out = dx + t * H;
+    const float mg = RMS ? 0.0f : sg * inv, mx = sx * inv;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if (i0 + j * G >= nv) continue;
+      if (!FULL && i0 + j * G >= nv) continue;
 #pragma unroll
-      for (int k = 0; k < N; ++k) gr[j][k] = rt * (gr[j][k] - mg - xh[j][k] * mx);
-      Row16<E>::store(dx, t * nv + i0 + j * G, gr[j]);
+      for (int k = 0; k < N; ++k) gr[j][k] = rt * fmaf(-xh[j][k], mx, RMS ? gr[j][k] : gr[j][k] - mg);
+      Row16<E>::store(out, i0 + j * G, gr[j]);
     }
   }
   ring.drain();
   if (!part) return;
-  // The groups' column sums are added in group order, through the ring's memory
-  // once every group is done with it. Element k of vector i is kept at k * nv + i,
-  // so that a warp's accesses fall into different banks.
-  if (groups > 1) __syncthreads();
-  float* col = reinterpret_cast<float*>(ring_mem);
-  float* out = part + static_cast<int64_t>(blockIdx.x) * 2 * H;
-  for (int turn = 0; turn < groups; ++turn) {
-    if (turn == g) {
+  // The groups' column sums meet in the ring's memory once every group is done
+  // with it, and are added in group order. Element k of vector i is kept at
+  // k * (nv + 32 / N) + i: a warp that writes one k of 32 vectors and a warp that
+  // reads 32 neighbouring columns both fall into 32 different banks.
+  float* const out_part = part + static_cast<int64_t>(blockIdx.x) * 2 * H;
+  if (groups == 1) {
 #pragma unroll
-      for (int j = 0; j < VPT; ++j) {
-        const int i = i0 + j * G;
-        if (i >= nv) continue;
+    for (int j = 0; j < VPT; ++j) {
+      const int i = i0 + j * G;
+      if (!FULL && i >= nv) continue;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          if (turn > 0) {
-            aw[j][k] = col[k * nv + i] + aw[j][k];
-            ab[j][k] = col[H + k * nv + i] + ab[j][k];
-          }
-          if (turn < groups - 1) {
-            col[k * nv + i] = aw[j][k];
-            col[H + k * nv + i] = ab[j][k];
-          }
-        }
-        if (turn == groups - 1) {
-#pragma unroll
-          for (int k = 0; k < N; k += 4) {
-            *reinterpret_cast<float4*>(out + i * N + k) = make_float4(aw[j][k], aw[j][k + 1], aw[j][k + 2], aw[j][k + 3]);
-            *reinterpret_cast<float4*>(out + H + i * N + k) =
-                make_float4(ab[j][k], ab[j][k + 1], ab[j][k + 2], ab[j][k + 3]);
-          }
-        }
+      for (int k = 0; k < N; k += 4) {
+        *reinterpret_cast<float4*>(out_part + i * N + k) = make_float4(aw[j][k], aw[j][k + 1], aw[j][k + 2], aw[j][k + 3]);
+        *reinterpret_cast<float4*>(out_part + H + i * N + k) =
+            make_float4(ab[j][k], ab[j][k + 1], ab[j][k + 2], ab[j][k + 3]);
       }
     }
-    if (groups > 1) __syncthreads();
+    return;
+  }
+  __syncthreads();
+  float* const all = reinterpret_cast<float*>(ring_mem);
+  const int pitch = nv + 32 / N, region = N * pitch;
+  float* const mine = all + g * 2 * region;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int i = i0 + j * G;
+    if (!FULL && i >= nv) continue;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      mine[k * pitch + i] = aw[j][k];
+      mine[region + k * pitch + i] = ab[j][k];
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < H; c += blockDim.x) {
+    const int from = (c & (N - 1)) * pitch + c / N;
+    float a = all[from], b = all[region + from];
+    for (int o = 1; o < groups; ++o) {
+      a += all[o * 2 * region + from];
+      b += all[o * 2 * region + region + from];
+    }
+    out_part[c] = a;
+    out_part[H + c] = b;
   }
 }
 
-// dw[i], db[i] (+)= the parts' sums: 32 columns a block, 16 threads a column that
-// take every 16th part, then a fixed tree.
+// dw and db (+)= the parts' sums. The parts are rows of 2 H floats; a block takes
+// 64 of these columns, 16 lanes of four by 32 threads that take every 32nd part
+// (all of its loads in flight at once), then a fixed tree.
 __global__ void __launch_bounds__(512)
     norm_sum_kernel(int H, int parts, int accumulate, const float* __restrict__ part, float* __restrict__ dw,
                     float* __restrict__ db) {
-  __shared__ float sh[2][16][33];
+  __shared__ float4 sh[32][16];
   grid_dep_launch();
   grid_dep_wait();
-  const int lane = static_cast<int>(threadIdx.x & 31), y = static_cast<int>(threadIdx.x >> 5);
-  const int i = static_cast<int>(blockIdx.x) * 32 + lane;
-  float a = 0.0f, b = 0.0f;
-  if (i < H)
+  const int x = static_cast<int>(threadIdx.x & 15), y = static_cast<int>(threadIdx.x >> 4);
+  const int c = (static_cast<int>(blockIdx.x) * 16 + x) * 4;   // H is a multiple of 4
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (c < 2 * H) {
 #pragma unroll 5
-    for (int p = y; p < parts; p += 16) {
-      a += part[static_cast<int64_t>(p) * 2 * H + i];
-      b += part[(static_cast<int64_t>(p) * 2 + 1) * H + i];
+    for (int p = y; p < parts; p += 32) {
+      const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p) * 2 * H + c);
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
     }
-  sh[0][y][lane] = a;
-  sh[1][y][lane] = b;
+  }
+  sh[y][x] = a;
   __syncthreads();
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = 16; o > 0; o >>= 1) {
     if (y < o) {
-      sh[0][y][lane] += sh[0][y + o][lane];
-      sh[1][y][lane] += sh[1][y + o][lane];
+      const float4 v = sh[y + o][x];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+      sh[y][x] = a;
     }
     __syncthreads();
   }
-  if (y == 0 && i < H) {
-    if (dw) dw[i] = accumulate ? dw[i] + sh[0][0][lane] : sh[0][0][lane];
-    if (db) db[i] = accumulate ? db[i] + sh[1][0][lane] : sh[1][0][lane];
+  float* out = c < H ? dw : db;
+  if (y != 0 || c >= 2 * H || !out) return;
+  float4* to = reinterpret_cast<float4*>(out + (c < H ? c : c - H));
+  if (accumulate) {
+    const float4 o = *to;
+    a = make_float4(o.x + a.x, o.y + a.y, o.z + a.z, o.w + a.w);
   }
+  *to = a;
 }
 
 // Rows too wide for registers (more than 4096 vectors forward, 1024 backward): one
@@ -480,26 +507,26 @@ __device__ __forceinline__ void store_f(float* p, int64_t i, float v) { p[i] = v
 __device__ __forceinline__ void store_f(__nv_bfloat16* p, int64_t i, float v) { p[i] = __float2bfloat16_rn(v); }
 
 template <typename E>
-__global__ void __launch_bounds__(kBwdThreads)
+__global__ void __launch_bounds__(kWideThreads)
     norm_wide_fwd_kernel(int H, int rms, const E* __restrict__ x, const E* __restrict__ w, const E* __restrict__ b,
                          float eps, E* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd) {
   __shared__ float sh[64];
   grid_dep_launch();
   grid_dep_wait();
-  GroupSum sum{sh, kBwdThreads, 1, 0};
+  GroupSum sum{sh, kWideThreads, 1, 0};
   const int64_t row = static_cast<int64_t>(blockIdx.x) * H;
   float mu = 0.0f, s = 0.0f;
   if (!rms) {
-    for (int i = threadIdx.x; i < H; i += kBwdThreads) s += load_f(x, row + i);
+    for (int i = threadIdx.x; i < H; i += kWideThreads) s += load_f(x, row + i);
     mu = sum(s) / static_cast<float>(H);
   }
   float q = 0.0f;
-  for (int i = threadIdx.x; i < H; i += kBwdThreads) {
+  for (int i = threadIdx.x; i < H; i += kWideThreads) {
     const float d = load_f(x, row + i) - mu;
     q = fmaf(d, d, q);
   }
   const float r = 1.0f / sqrtf(sum(q) / static_cast<float>(H) + eps);
-  for (int i = threadIdx.x; i < H; i += kBwdThreads) {
+  for (int i = threadIdx.x; i < H; i += kWideThreads) {
     float v = (load_f(x, row + i) - mu) * r;
     if (w) v *= load_f(w, i);
     if (b) v += load_f(b, i);
@@ -512,24 +539,24 @@ __global__ void __launch_bounds__(kBwdThreads)
 }
 
 template <typename E, typename D>
-__global__ void __launch_bounds__(kBwdThreads)
+__global__ void __launch_bounds__(kWideThreads)
     norm_wide_dx_kernel(int H, int rms, const E* __restrict__ x, const E* __restrict__ w, const D* __restrict__ dy,
                         const float* __restrict__ mean, const float* __restrict__ rstd, E* __restrict__ dx) {
   __shared__ float sh[64];
   grid_dep_launch();
   grid_dep_wait();
-  GroupSum sum{sh, kBwdThreads, 1, 0};
+  GroupSum sum{sh, kWideThreads, 1, 0};
   const int64_t row = static_cast<int64_t>(blockIdx.x) * H;
   const float mu = rms ? 0.0f : mean[blockIdx.x], r = rstd[blockIdx.x];
   float sg = 0.0f, sx = 0.0f;
-  for (int i = threadIdx.x; i < H; i += kBwdThreads) {
+  for (int i = threadIdx.x; i < H; i += kWideThreads) {
     const float g = load_f(dy, row + i) * (w ? load_f(w, i) : 1.0f);
     sg += g;
     sx = fmaf(g, (load_f(x, row + i) - mu) * r, sx);
   }
   const float mg = rms ? 0.0f : sum(sg) / static_cast<float>(H);
   const float mx = sum(sx) / static_cast<float>(H);
-  for (int i = threadIdx.x; i < H; i += kBwdThreads) {
+  for (int i = threadIdx.x; i < H; i += kWideThreads) {
     const float g = load_f(dy, row + i) * (w ? load_f(w, i) : 1.0f);
     store_f(dx, row + i, r * (g - mg - (load_f(x, row + i) - mu) * r * mx));
   }
@@ -570,7 +597,7 @@ struct Shape {
   size_t smem;
 };
 Shape shape(const vce_problem& p, int most, int cap_threads, int64_t slot_bytes, int64_t fixed_bytes,
-            int64_t min_smem) {
+            int64_t min_smem) {   // min_smem: a group
   Shape s{};
   const int64_t nv = p.H / (p.dtype == VCE_BF16 ? 8 : 4);
   const int64_t sms = current_device_info().num_sms;
@@ -592,7 +619,7 @@ Shape shape(const vce_problem& p, int most, int cap_threads, int64_t slot_bytes,
   const int64_t rows = s.fused ? ceil_div(p.T, groups) : p.T;
   s.ctas = static_cast<int>(rows < sms ? rows : sms);
   s.smem = static_cast<size_t>(groups * s.slots * slot_bytes + fixed_bytes);
-  if (s.smem < static_cast<size_t>(min_smem)) s.smem = static_cast<size_t>(min_smem);
+  if (s.smem < static_cast<size_t>(min_smem * groups)) s.smem = static_cast<size_t>(min_smem * groups);
   return s;
 }
 Shape fwd_shape(const vce_problem& p) {
@@ -601,7 +628,7 @@ Shape fwd_shape(const vce_problem& p) {
 }
 Shape bwd_shape(const vce_problem& p) {
   const int64_t row = p.H * ((p.dtype == VCE_BF16 ? 2 : 4) + ((p.flags & VCE_FLAG_DH_BF16) ? 2 : 4));
-  return shape(p, 2, kBwdThreads, row, 0, 2 * p.H * static_cast<int64_t>(sizeof(float)));
+  return shape(p, 4, kBwdThreads, row, 0, (2 * p.H + 64) * static_cast<int64_t>(sizeof(float)));
 }
 
 // Raises the kernel's shared-memory limit once per device, then launches it.
@@ -644,7 +671,7 @@ cudaError_t fwd_typed(const vce_problem& p, bool rms, const void* x_, const void
   const int64_t nv = p.H / Row16<E>::N, vpt = ceil_div(nv, s.G);
   cudaError_t e;
   if (!s.fused)
-    e = launch_dependent(norm_wide_fwd_kernel<E>, dim3(static_cast<unsigned>(p.T)), dim3(kBwdThreads), 0, st,
+    e = launch_dependent(norm_wide_fwd_kernel<E>, dim3(static_cast<unsigned>(p.T)), dim3(kWideThreads), 0, st,
                          static_cast<int>(p.H), rms ? 1 : 0, x, w, b, eps, y, mean, rstd);
   else
     e = vpt <= 1   ? fwd_vpt<E, 1>(p, s, rms, x, w, b, eps, y, mean, rstd, status, st)
@@ -655,12 +682,20 @@ cudaError_t fwd_typed(const vce_problem& p, bool rms, const void* x_, const void
   return e;
 }
 
+template <typename E, typename D, int VPT, bool RMS, bool FULL>
+cudaError_t bwd_as(const vce_problem& p, const Shape& s, const E* x, const E* w, const D* dy, const float* mean,
+                   const float* rstd, E* dx, float* part, int32_t* status, cudaStream_t st) {
+  static std::atomic<uint64_t> configured{0};
+  return launch_ring(norm_bwd_kernel<E, D, VPT, RMS, FULL>, configured, s, st, p.T, static_cast<int>(p.H), s.G, s.slots,
+                     x, w, dy, mean, rstd, dx, part, status, wait_limit_ns());
+}
 template <typename E, typename D, int VPT>
 cudaError_t bwd_vpt(const vce_problem& p, const Shape& s, bool rms, const E* x, const E* w, const D* dy,
                     const float* mean, const float* rstd, E* dx, float* part, int32_t* status, cudaStream_t st) {
-  static std::atomic<uint64_t> configured{0};
-  return launch_ring(norm_bwd_kernel<E, D, VPT>, configured, s, st, p.T, static_cast<int>(p.H), s.G, s.slots,
-                     rms ? 1 : 0, x, w, dy, mean, rstd, dx, part, status, wait_limit_ns());
+  const bool full = p.H == static_cast<int64_t>(VPT) * s.G * Row16<E>::N;
+  auto go = [&](auto f) { return f(p, s, x, w, dy, mean, rstd, dx, part, status, st); };
+  return rms ? (full ? go(bwd_as<E, D, VPT, true, true>) : go(bwd_as<E, D, VPT, true, false>))
+             : (full ? go(bwd_as<E, D, VPT, false, true>) : go(bwd_as<E, D, VPT, false, false>));
 }
 template <typename E, typename D>
 cudaError_t bwd_typed(const vce_problem& p, bool rms, const void* x_, const void* w_, const void* dy_,
@@ -675,13 +710,15 @@ cudaError_t bwd_typed(const vce_problem& p, bool rms, const void* x_, const void
   const bool sums = dw || db;
   cudaError_t e = cudaSuccess;
   if (s.fused) {
-    const bool one = p.H / Row16<E>::N <= s.G;
-    e = one ? bwd_vpt<E, D, 1>(p, s, rms, x, w, dy, mean, rstd, dx, sums ? part : nullptr, status, st)
-            : bwd_vpt<E, D, 2>(p, s, rms, x, w, dy, mean, rstd, dx, sums ? part : nullptr, status, st);
+    const int64_t vpt = ceil_div(p.H / Row16<E>::N, s.G);
+    float* to = sums ? part : nullptr;
+    e = vpt <= 1   ? bwd_vpt<E, D, 1>(p, s, rms, x, w, dy, mean, rstd, dx, to, status, st)
+        : vpt <= 2 ? bwd_vpt<E, D, 2>(p, s, rms, x, w, dy, mean, rstd, dx, to, status, st)
+                   : bwd_vpt<E, D, 4>(p, s, rms, x, w, dy, mean, rstd, dx, to, status, st);
     note_launch(VCE_K_NORM_BWD, st);
   } else {
     if (dx) {
-      e = launch_dependent(norm_wide_dx_kernel<E, D>, dim3(static_cast<unsigned>(p.T)), dim3(kBwdThreads), 0, st, H,
+      e = launch_dependent(norm_wide_dx_kernel<E, D>, dim3(static_cast<unsigned>(p.T)), dim3(kWideThreads), 0, st, H,
                            rms ? 1 : 0, x, w, dy, mean, rstd, dx);
       note_launch(VCE_K_NORM_BWD, st);
     }
