@@ -567,7 +567,7 @@ typedef enum vce_kernel_kind {
   VCE_K_TC_ARGMAX = 17, VCE_K_ARGMAX_MERGE = 18, VCE_K_SIMT_ARGMAX = 19,
   VCE_K_NGRAM_HASH = 20, VCE_K_NGRAM_FWD = 21, VCE_K_EMBED_HDR = 22, VCE_K_DH_BF16 = 23,
   VCE_K_EMBED_SORT_CLUSTER = 24, VCE_K_TC_SCORE = 25, VCE_K_SCORE_ROWS = 26, VCE_K_TC_SCORE_GRAD = 27,
-  VCE_K_SIMT_LOGITS = 28, VCE_K_SIMT_SCORE_GRAD = 29, VCE_K_MASK_ROWS = 30, VCE_K_NORM_FWD = 31,
+  VCE_K_SIMT_LOGITS = 28, VCE_K_SIMT_SCORE_GRAD = 29, VCE_K_DH_JOIN = 30, VCE_K_NORM_FWD = 31,
   VCE_K_NORM_BWD = 32, VCE_K_NORM_SUM = 33, VCE_K_SCORE_DECODE = 34, VCE_K_SCORE_MERGE = 35,
   VCE_K_SCORE_LISTS = 36, VCE_K_SCORE_ZERO = 37
 } vce_kernel_kind;

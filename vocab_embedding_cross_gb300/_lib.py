@@ -395,7 +395,7 @@ KERNEL_KINDS = ["embed_gather", "embed_sort", "embed_reduce", "tc_fwd", "tc_grad
                 "merge", "loss_mean", "count_valid", "simt_fwd", "simt_grad", "sgemm", "wait_selftest",
                 "dh_reduce", "sampled_cand", "sampled_scatter", "tc_argmax", "argmax_merge", "simt_argmax",
                 "ngram_hash", "ngram_fwd", "embed_hdr", "dh_bf16", "embed_sort_cluster", "tc_score", "score_rows",
-                "tc_score_grad", "simt_logits", "simt_score_grad", "mask_rows", "norm_fwd", "norm_bwd", "norm_sum",
+                "tc_score_grad", "simt_logits", "simt_score_grad", "dh_join", "norm_fwd", "norm_bwd", "norm_sum",
                 "score_decode", "score_merge", "score_lists", "score_zero"]
 
 

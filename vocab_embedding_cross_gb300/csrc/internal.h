@@ -85,6 +85,16 @@ struct ScoreGrad {
   float scale;   // logits are scale * <h, W>
 };
 
+// The tensor-core scores' backward beside the loss's: hm receives h without the
+// rows of tokens that have no gradient (null: every token has one); P, where dH is
+// made in parts, holds dh_parts of them, [part][T rounded up to 256][H].
+struct ScoreBwd {
+  ScoreGrad sg;
+  void* hm;
+  float* P;
+  bool dW_bf16;
+};
+
 // Statistics and lists of alternatives of the tensor-core scores.
 struct ScoreLists {
   float scale;
@@ -202,10 +212,6 @@ cudaError_t launch_simt_argmax(const ProbDev& pd, const UnitGrid& ug, const floa
 cudaError_t launch_simt_grad(const ProbDev& pd, const float* h, const float* W, const int64_t* targets,
                              const float* lse, const int32_t* n_valid, float g, int v0, int vc, float* G,
                              cudaStream_t st);
-cudaError_t launch_simt_logits(const ProbDev& pd, const float* h, const float* W, float* Z, int64_t ldz,
-                               cudaStream_t st);
-cudaError_t launch_simt_score_grad(const ProbDev& pd, const float* h, const float* W, const int64_t* targets,
-                                   const ScoreGrad& sg, int v0, int vc, float* G, cudaStream_t st);
 // C[M,N] = beta*C + sum_k A(m,k) B(k,n), A(m,k) = A[m*sam + k*sak], B(k,n) = B[k*sbk + n*sbn],
 // C row-major with leading dimension ldc. beta is 0 or 1.
 cudaError_t launch_sgemm(int M, int N, int K, const float* A, int64_t sam, int64_t sak, const float* B,
@@ -221,7 +227,9 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
                                 const float* lse, float g, int v0, int vc_act,
                                 void* G, int g_ld, float* dH, bool dH_accumulate, void* dW, bool dW_accumulate,
                                 int32_t* dh_flags, int dh_parts, int32_t* status, cudaStream_t st,
-                                const ScoreGrad* sg = nullptr, bool dW_bf16 = false);
+                                const ScoreBwd* sb = nullptr);
+// Parts of the scores' dH that are stored on their own and joined; 1: none.
+int tc_dh_stored_parts(const vce_problem& p);
 // Per (token, unit) statistics into sl.part, target logits into ztgt and, for
 // sl.K > 0, the lists that launch_score_lists takes the alternatives from;
 // sl.slots, sl.bound and sl.row_count must be zero.
@@ -268,9 +276,18 @@ cudaError_t launch_score_decode(const vce_problem& p, const void* h, const void*
                                 float scale, int K, float* logp, float* entropy, float* lse, int64_t* top_ids,
                                 float* top_logp, void* ws, int32_t* status, cudaStream_t st);
 cudaError_t launch_zero_words(void* p, size_t bytes, cudaStream_t st);   // bytes: a multiple of 16
-// out = h with the rows of tokens without a real target set to zero.
-cudaError_t launch_mask_rows(const void* h, const int64_t* targets, int64_t T, int V, int64_t ignore_index,
-                             int64_t row_bytes, void* out, int32_t* status, cudaStream_t st);
+// fp32 scores (score_f32.cu). The backward of one column chunk: G[T, vc] (row
+// stride ldg), dH (+)= G W or, with parts > 1, its parts into P[part][T][H], and
+// dW[v0..] (+)= G^T h.
+int f32_dh_parts(int64_t T, int64_t H, int64_t K);
+cudaError_t launch_f32_logits(const ProbDev& pd, const float* h, const float* W, float* Z, int64_t ldz,
+                              cudaStream_t st);
+cudaError_t launch_f32_score_bwd(const ProbDev& pd, const float* h, const float* W, const int64_t* targets,
+                                 const ScoreGrad& sg, int v0, int vc, float* G, int64_t ldg, float* P, int parts,
+                                 float* dH, bool dH_add, float* dW, bool dW_add, int32_t* status, cudaStream_t st);
+// out[0..n) (+)= before + the parts in order (fp32 or bf16; n a multiple of 4; before may be null).
+cudaError_t launch_join(const float* P, int64_t part_elems, int parts, const float* before, bool add, void* out,
+                        bool out_bf16, int64_t n, cudaStream_t st);
 
 // Layer and RMS normalisation (norm.cu).
 size_t norm_ws_bytes(const vce_problem& p);

@@ -234,73 +234,6 @@ __global__ void __launch_bounds__(256) simt_grad_kernel(ProbDev pd, const float*
   }
 }
 
-// grid (ceil(T/64), column blocks of 64, at most 65535): Z[t, v] = z_tv for the real columns.
-__global__ void __launch_bounds__(256) simt_logits_kernel(ProbDev pd, const float* __restrict__ h,
-                                                          const float* __restrict__ W, float* __restrict__ Z,
-                                                          int64_t ldz) {
-  __shared__ float hs[TK][TM + 4];
-  __shared__ float ws[TK][TN + 4];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int m0 = blockIdx.x * TM;
-  for (int64_t vt0 = static_cast<int64_t>(blockIdx.y) * TN; vt0 < pd.V_real;
-       vt0 += static_cast<int64_t>(gridDim.y) * TN) {
-    float acc[4][4];
-    z_tile(h, W, pd.T, pd.H, m0, vt0, pd.V_real, acc, hs, ws);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = m0 + 4 * ty + i;
-      if (r >= pd.T) continue;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t v = vt0 + 4 * tx + j;
-        if (v < pd.V_real) Z[r * ldz + v] = acc[i][j];
-      }
-    }
-  }
-}
-
-// grid (ceil(T/64), ceil(vc/64)): the token scores' gradient with respect to
-// the unscaled logits, G[t, v - v0] = s (g_logp ([v == y] - p) - g_entropy p
-// (logp + entropy)) with logp = s z - lse and p = exp(logp); 0 for tokens
-// without a valid target (targets != NULL).
-__global__ void __launch_bounds__(256) simt_score_grad_kernel(ProbDev pd, const float* __restrict__ h,
-                                                              const float* __restrict__ W,
-                                                              const int64_t* __restrict__ targets, ScoreGrad sg,
-                                                              int v0, int vc, float* __restrict__ G) {
-  __shared__ float hs[TK][TM + 4];
-  __shared__ float ws[TK][TN + 4];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int m0 = blockIdx.x * TM;
-  const int64_t vt0 = v0 + static_cast<int64_t>(blockIdx.y) * TN;
-  const int64_t vend = static_cast<int64_t>(v0) + vc;
-  const int64_t vlim = vend < pd.V_real ? vend : pd.V_real;
-  float acc[4][4];
-  z_tile(h, W, pd.T, pd.H, m0, vt0, vlim, acc, hs, ws);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = m0 + 4 * ty + i;
-    if (r >= pd.T) continue;
-    const int64_t y = targets ? targets[r] : -1;
-    const bool row_ok = targets ? (y >= 0 && y < pd.V_real) : true;
-    const float lse = sg.lse[r];
-    const float gl = sg.g_logp ? sg.g_logp[r] : 0.0f;
-    const float ge = sg.g_entropy ? sg.g_entropy[r] : 0.0f;
-    const float off = sg.g_entropy ? sg.entropy[r] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t v = vt0 + 4 * tx + j;
-      if (v >= vend) continue;
-      float gv = 0.0f;
-      if (row_ok && v < pd.V_real) {
-        const float lp = fmaf(acc[i][j], sg.scale, -lse);
-        const float p = expf(lp);
-        gv = sg.scale * (gl * ((v == y ? 1.0f : 0.0f) - p) - ge * p * (lp + off));
-      }
-      G[static_cast<int64_t>(r) * vc + (v - v0)] = gv;
-    }
-  }
-}
-
 __global__ void __launch_bounds__(256) sgemm_kernel(int M, int N, int K, const float* __restrict__ A, int64_t sam,
                                                     int64_t sak, const float* __restrict__ B, int64_t sbk,
                                                     int64_t sbn, float* __restrict__ C, int64_t ldc, int beta) {
@@ -381,23 +314,6 @@ cudaError_t launch_simt_grad(const ProbDev& pd, const float* h, const float* W, 
   dim3 grid(static_cast<unsigned>(ceil_div(pd.T, TM)), static_cast<unsigned>(ceil_div(vc, TN)));
   simt_grad_kernel<<<grid, 256, 0, st>>>(pd, h, W, targets, lse, n_valid, g, v0, vc, G);
   note_launch(VCE_K_SIMT_GRAD, st);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_simt_logits(const ProbDev& pd, const float* h, const float* W, float* Z, int64_t ldz,
-                               cudaStream_t st) {
-  const int64_t nb = ceil_div(pd.V_real, TN);
-  dim3 grid(static_cast<unsigned>(ceil_div(pd.T, TM)), static_cast<unsigned>(nb < 65535 ? nb : 65535));
-  simt_logits_kernel<<<grid, 256, 0, st>>>(pd, h, W, Z, ldz);
-  note_launch(VCE_K_SIMT_LOGITS, st);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_simt_score_grad(const ProbDev& pd, const float* h, const float* W, const int64_t* targets,
-                                   const ScoreGrad& sg, int v0, int vc, float* G, cudaStream_t st) {
-  dim3 grid(static_cast<unsigned>(ceil_div(pd.T, TM)), static_cast<unsigned>(ceil_div(vc, TN)));
-  simt_score_grad_kernel<<<grid, 256, 0, st>>>(pd, h, W, targets, sg, v0, vc, G);
-  note_launch(VCE_K_SIMT_SCORE_GRAD, st);
   return cudaGetLastError();
 }
 

@@ -124,7 +124,10 @@ struct TcArgs {
   int32_t* status;
   uint64_t limit_ns;
   int32_t* merge_ctr;   // FWD: the merge's block counter, zeroed here for the merge that follows
+  int part_rows;        // DH: 0, or part k of K is stored on its own, at row k * part_rows
   ScoreGrad sg;         // SGRAD: what the forward scores left and their upstream gradients
+  const uint4* h16;     // SGRAD: h, and where it is copied without the rows of tokens
+  uint4* hm16;          // that have no gradient (or null)
   ScoreLists sl;        // SCORE: statistics, scale and the lists of alternatives
 };
 
@@ -646,6 +649,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (bad && lane == 0 && blockIdx.x == 0) record_status(a.status, VCE_ERR_BAD_INDEX);
       scale = nv > 0 ? a.g / static_cast<float>(nv) : 0.0f;
     }
+    if constexpr (MODE == MODE_SGRAD) {
+      // While the first tile's MMAs run: h without the rows that have no gradient,
+      // for G^T h, which must not multiply a zero of G by what such a row holds.
+      if (a.hm16) {
+        const int row16 = a.pd.H / 8;
+        const int64_t n16 = static_cast<int64_t>(a.pd.T) * row16;
+        const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kEpiWarps);
+        for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * (32 * kEpiWarps) + threadIdx.x - 64; i0 < n16;
+             i0 += 4 * step) {
+          uint4 v[4];
+          bool take[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t i = i0 + j * step;
+            const int64_t y = i < n16 ? __ldg(a.targets + i / row16) : a.pd.ignore_index;
+            take[j] = y >= 0 && y < a.pd.V_real;
+            if (!take[j] && y != a.pd.ignore_index) record_status(a.status, VCE_ERR_BAD_INDEX);
+            if (i < n16) v[j] = __ldg(a.h16 + i);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (i0 + j * step < n16) a.hm16[i0 + j * step] = take[j] ? v[j] : make_uint4(0, 0, 0, 0);
+        }
+      }
+    }
     auto release = [&](uint32_t acc) {
       tc_fence_before();
       __syncwarp();
@@ -1076,7 +1104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           n_blk = item % a.n_nblk;
           m_blk = (item / a.n_nblk) % a.n_mblk;
           part = (item / a.n_nblk) / a.n_mblk;   // DH: this item's K part
-          row0 = (kDwLike<MODE> ? a.out_row0 : 0) + m_blk * BMP + static_cast<int>(rank) * BM;
+          row0 = (kDwLike<MODE> ? a.out_row0 : (MODE == MODE_DH ? part * a.part_rows : 0)) + m_blk * BMP + static_cast<int>(rank) * BM;
           col0 = n_blk * BN + half * 128;
         }
         const int orow = row0 + q * 32;
@@ -1092,14 +1120,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // order, so the sum dH (+)= P0 + P1 + ... is the same at every run.
           // Parts are numbered part-major, so part k - 1 of this tile ran a
           // wave earlier and its count is normally there already.
-          if (a.ksplit > 1) {
+          if (a.ksplit > 1 && !a.part_rows) {
             flag = a.dh_flags + ((m_blk * a.n_nblk + n_blk) * 2 + static_cast<int>(rank)) * kEpiWarps + e;
             if (part > 0 && !flag_wait_ge(flag, part, lane, wc)) {
               ok = false;
               break;
             }
           }
-          add_out = a.accumulate || part > 0;
+          add_out = a.accumulate || (part > 0 && !a.part_rows);
         }
         const uint32_t ta = lane_base + acc * BN;
         if constexpr (MODE == MODE_GRAD) {
@@ -1399,6 +1427,18 @@ int tc_unit_width(const vce_problem& p) {
   return best_uw;
 }
 
+int tc_dh_stored_parts(const vce_problem& p) {
+  // Where the parts that are added in turn (at most kMaxDhParts a tile) leave
+  // clusters without work: as many as make one wave, each with 16 K blocks or more.
+  const int64_t clusters = current_device_info().num_sms / 2;
+  const int64_t tiles = ceil_div(p.T, BMP) * ceil_div(p.H, BN);
+  if (tiles * kMaxDhParts >= 2 * clusters) return 1;
+  int64_t parts = clusters / tiles;
+  const int64_t kb = ceil_div(p.V_real, BK);
+  if (parts > kb / 16) parts = kb / 16;
+  return parts < 2 ? 1 : static_cast<int>(parts);
+}
+
 int tc_dh_parts(const vce_problem& p, int vc_act) {
   const DevInfo di = current_device_info();
   const int clusters = max_clusters<MODE_DH>(di);
@@ -1489,8 +1529,11 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
                                 const float* lse, float g, int v0, int vc_act, void* G,
                                 int g_ld, float* dH, bool dH_accumulate, void* dW, bool dW_accumulate,
                                 int32_t* dh_flags, int dh_parts, int32_t* status, cudaStream_t st,
-                                const ScoreGrad* sg, bool dW_bf16) {
-  const int parts = dh_flags ? dh_parts : 1;
+                                const ScoreBwd* sb) {
+  const bool dW_bf16 = sb && sb->dW_bf16;
+  float* const P = sb ? sb->P : nullptr;
+  const int64_t part_rows = ceil_div(p.T, BMP) * BMP;
+  const int parts = dh_flags || P ? dh_parts : 1;
   const int n_flags = static_cast<int>(ceil_div(p.T, BMP) * ceil_div(p.H, BN)) * 2 * kEpiWarps;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto F32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
@@ -1514,9 +1557,11 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     a.v0 = v0;
     a.vc = vc_act;
     a.dh_flags = parts > 1 ? dh_flags : nullptr;
-    a.n_dh_flags = parts > 1 ? n_flags : 0;
-    if (sg) {
-      a.sg = *sg;
+    a.n_dh_flags = parts > 1 && dh_flags ? n_flags : 0;
+    if (sb) {
+      a.sg = sb->sg;
+      a.h16 = static_cast<const uint4*>(h);
+      a.hm16 = v0 == 0 ? static_cast<uint4*>(sb->hm) : nullptr;   // once, with the first column chunk
       e = launch_mode<MODE_SGRAD>(mh, mw, mg, a, st);
     } else {
       e = launch_mode<MODE_GRAD>(mh, mw, mg, a, st);
@@ -1530,7 +1575,7 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     CUtensorMap mg, mw, mo;
     if (!make_tmap_2d(&mg, G, BF, 2, vc_act, p.T, g_ld, 64, BM, true) ||
         !make_tmap_2d(&mw, W, BF, 2, p.H, p.V_real, p.H, 64, 64, true) ||
-        !make_tmap_2d(&mo, dH, F32, 4, p.H, p.T, p.H, 32, 32, true))
+        !make_tmap_2d(&mo, P ? P : dH, F32, 4, p.H, P ? part_rows * parts : p.T, p.H, 32, 32, true))
       return cudaErrorInvalidValue;
     TcArgs a = base_args(p, targets, status);
     a.n_mblk = static_cast<int>(ceil_div(p.T, BMP));
@@ -1539,17 +1584,18 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     a.ksplit = parts;
     a.kb_per = static_cast<int>(ceil_div(a.num_kb, parts));
     a.dh_flags = parts > 1 ? dh_flags : nullptr;
-    a.n_dh_flags = parts > 1 ? n_flags : 0;
+    a.n_dh_flags = parts > 1 && dh_flags ? n_flags : 0;
     a.n_items = a.n_mblk * parts * a.n_nblk;
     a.v0 = v0;
-    a.accumulate = dH_accumulate ? 1 : 0;
+    a.part_rows = P ? static_cast<int>(part_rows) : 0;
+    a.accumulate = dH_accumulate && !P ? 1 : 0;
     if ((e = launch_mode<MODE_DH>(mg, mw, mo, a, st)) != cudaSuccess) return e;
   }
   // DW: dW[v0:v0+vc_act, :] (+)= G[:, 0:vc_act]^T h
   {
     CUtensorMap mg, mh, mo;
     if (!make_tmap_2d(&mg, G, BF, 2, vc_act, p.T, g_ld, 64, 64, true) ||
-        !make_tmap_2d(&mh, h, BF, 2, p.H, p.T, p.H, 64, 64, true) ||
+        !make_tmap_2d(&mh, sb && sb->hm ? sb->hm : h, BF, 2, p.H, p.T, p.H, 64, 64, true) ||
         !make_tmap_2d(&mo, dW, dW_bf16 ? BF : F32, dW_bf16 ? 2 : 4, p.H, static_cast<uint64_t>(v0) + vc_act, p.H,
                       dW_bf16 ? 64 : 32, 32, true))
       return cudaErrorInvalidValue;

@@ -111,24 +111,6 @@ __global__ void __launch_bounds__(256) zero_words_kernel(uint4* __restrict__ p, 
     p[i] = make_uint4(0, 0, 0, 0);
 }
 
-// Rows of h whose token takes part in the gradient, zeros for the others: the
-// product G^T h then never multiplies a zero of G by what an ignored token's
-// row holds (which may be infinite or NaN). Targets that are neither a real
-// class nor ignored are reported.
-__global__ void __launch_bounds__(256) mask_rows_kernel(const uint4* __restrict__ h, const int64_t* __restrict__ targets,
-                                                        int V, int64_t ignore_index, int row16, int64_t n16, uint4* __restrict__ out,
-                                                        int32_t* status) {
-  grid_dep_launch();
-  grid_dep_wait();
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n16;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t y = targets[i / row16];
-    const bool valid = y >= 0 && y < V;
-    if (!valid && y != ignore_index && status) atomicCAS(status, 0, static_cast<int>(VCE_ERR_BAD_INDEX));
-    out[i] = valid ? h[i] : make_uint4(0, 0, 0, 0);
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_score_rows(const float* Z, int64_t ldz, int64_t rows, int V, const int64_t* targets,
@@ -157,19 +139,6 @@ cudaError_t launch_zero_words(void* p, size_t bytes, cudaStream_t st) {
   const cudaError_t e = launch_dependent(zero_words_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)),
                                          dim3(256), 0, st, static_cast<uint4*>(p), n16);
   note_launch(VCE_K_SCORE_ZERO, st);
-  return e;
-}
-
-cudaError_t launch_mask_rows(const void* h, const int64_t* targets, int64_t T, int V, int64_t ignore_index,
-                             int64_t row_bytes, void* out, int32_t* status, cudaStream_t st) {
-  const int64_t n16 = T * (row_bytes / 16);
-  const int64_t cap = static_cast<int64_t>(current_device_info().num_sms) * 8;
-  const int64_t want = ceil_div(n16, 256);
-  const cudaError_t e = launch_dependent(mask_rows_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)),
-                                         dim3(256), 0, st, static_cast<const uint4*>(h), targets, V,
-                                         ignore_index, static_cast<int>(row_bytes / 16), n16,
-                                         static_cast<uint4*>(out), status);
-  note_launch(VCE_K_MASK_ROWS, st);
   return e;
 }
 

@@ -253,9 +253,26 @@ size_t score_ws_bytes(const vce_problem& p, int K) {
   const size_t a = score_pass_bytes(q, K), b = r.T > 0 ? score_pass_bytes(r, K) : 0;
   return kWsAlign + (a > b ? a : b);
 }
-// The backward's copy of h without the rows of ignored tokens.
-size_t masked_h_bytes(const vce_problem& p) {
-  return align_up(static_cast<size_t>(p.T) * static_cast<size_t>(p.H) * g_esize(p), kWsAlign);
+// The backward: in front of the header, the G chunk and the dH counters (laid out
+// as the loss backward's) stand the fp32 sum of a bf16 dH, the bf16 path's copy of
+// h without the rows of ignored tokens, and the parts of a dH with few tiles.
+struct ScoreBwdLayout {
+  size_t acc, hm, P, front;
+  int parts;
+  int64_t part_elems;
+};
+ScoreBwdLayout score_bwd_layout(const vce_problem& p) {
+  ScoreBwdLayout L{};
+  const size_t T = static_cast<size_t>(p.T), H = static_cast<size_t>(p.H);
+  const bool bf16 = p.dtype == VCE_BF16;
+  L.parts = p.T == 0 ? 1 : bf16 ? tc_dh_stored_parts(p) : f32_dh_parts(p.T, p.H, p.V_real);
+  const size_t rows = bf16 ? (T + 255) / 256 * 256 : T;
+  L.part_elems = static_cast<int64_t>(rows * H);
+  L.acc = 0;
+  L.hm = dh_acc_bytes(p);
+  L.P = L.hm + (bf16 ? align_up(T * H * 2, kWsAlign) : 0);
+  L.front = L.P + (L.parts > 1 ? align_up(static_cast<size_t>(L.parts) * rows * H * 4, kWsAlign) : 0);
+  return L;
 }
 
 // ----- sampled softmax: the sub-problems and the workspace layout -----
@@ -378,7 +395,7 @@ size_t vce_workspace_size(const vce_problem* p, int32_t op) {
     case VCE_OP_SAMPLED_CANDIDATES: return sampled_ws_bytes(*p);
     case VCE_OP_GREEDY_ARGMAX: return argmax_ws_bytes(*p);
     case VCE_OP_LOGPROB_BWD:
-      return dh_acc_bytes(*p) + masked_h_bytes(*p) + bwd_bytes_for(*p, bwd_recommended_cols(*p)) + dh_flag_bytes(*p);
+      return score_bwd_layout(*p).front + bwd_bytes_for(*p, bwd_recommended_cols(*p)) + dh_flag_bytes(*p);
     case VCE_OP_NORM_BWD: return norm_ws_bytes(*p);
   }
   return SIZE_MAX;
@@ -388,7 +405,7 @@ size_t vce_workspace_size_min(const vce_problem* p, int32_t op) {
   if (check_problem(p) != VCE_OK) return SIZE_MAX;
   if (op == VCE_OP_LOSS_BWD) return dh_acc_bytes(*p) + bwd_bytes_for(*p, p->T == 0 ? 0 : 256);
   if (op == VCE_OP_LOGPROB_BWD)
-    return dh_acc_bytes(*p) + masked_h_bytes(*p) + bwd_bytes_for(*p, p->T == 0 ? 0 : 256);
+    return score_bwd_layout(*p).front + bwd_bytes_for(*p, p->T == 0 ? 0 : 256);
   return vce_workspace_size(p, op);
 }
 
@@ -713,7 +730,7 @@ vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, c
                                at(lse), ids, tlp, status, st);
     } else {
       float* Z = reinterpret_cast<float*>(b);
-      e = launch_simt_logits(prob_dev(q), reinterpret_cast<const float*>(hr), static_cast<const float*>(W), Z, p->Vp,
+      e = launch_f32_logits(prob_dev(q), reinterpret_cast<const float*>(hr), static_cast<const float*>(W), Z, p->Vp,
                              st);
       if (e == cudaSuccess)
         e = launch_score_rows(Z, p->Vp, q.T, V, at(targets), p->ignore_index, logit_scale, n_top, at(logp),
@@ -747,60 +764,63 @@ vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, c
       !aligned(g_logp, 4) || !aligned(g_entropy, 4) || !aligned(dH_out, 16) || !aligned(dW, 16))
     return VCE_ERR_UNSUPPORTED;
   if (!ws || !aligned(ws, kWsAlign)) return VCE_ERR_WORKSPACE;
-  // Layout: fp32 sum of a bf16 dH | masked h | header | dH K-part counters | G chunk.
-  const size_t acc_bytes = dh_acc_bytes(*p), front = acc_bytes + masked_h_bytes(*p);
-  if (ws_bytes < front) return VCE_ERR_WORKSPACE;
-  float* dH = acc_bytes ? static_cast<float*>(ws) : static_cast<float*>(dH_out);
-  void* hm = static_cast<char*>(ws) + acc_bytes;
-  char* b = static_cast<char*>(ws) + front;
-  ws_bytes -= front;
-  const size_t part_bytes = dh_flag_bytes(*p);
-  const bool use_parts = part_bytes > 0 && ws_bytes >= bwd_bytes_for(*p, 256) + part_bytes;
-  int64_t vc = bwd_chunk_cols(*p, use_parts ? ws_bytes - part_bytes : ws_bytes);
+  const ScoreBwdLayout L = score_bwd_layout(*p);
+  if (ws_bytes < L.front) return VCE_ERR_WORKSPACE;
+  char* front = static_cast<char*>(ws);
+  char* b = front + L.front;
+  ws_bytes -= L.front;
+  const bool bf16 = p->dtype == VCE_BF16, dH_bf16 = (p->flags & VCE_FLAG_DH_BF16) != 0;
+  const size_t part_bytes = L.parts > 1 ? 0 : dh_flag_bytes(*p);
+  const bool use_flags = part_bytes > 0 && ws_bytes >= bwd_bytes_for(*p, 256) + part_bytes;
+  int64_t vc = bwd_chunk_cols(*p, use_flags ? ws_bytes - part_bytes : ws_bytes);
   if (vc < 256) return VCE_ERR_WORKSPACE;
-  if (vc > (int64_t(1) << 21)) vc = int64_t(1) << 21;   // the fp32 kernels' grids count 64-column blocks in 16 bits
   int32_t* status = dev_status;   // may be null: data errors then go unreported
-  int32_t* dh_flags = use_parts ? reinterpret_cast<int32_t*>(b + kBwdHeader) : nullptr;
-  void* G = b + kBwdHeader + (use_parts ? part_bytes : 0);
+  int32_t* dh_flags = use_flags ? reinterpret_cast<int32_t*>(b + kBwdHeader) : nullptr;
+  void* G = b + kBwdHeader + (use_flags ? part_bytes : 0);
   const ProbDev pd = prob_dev(*p);
   const ScoreGrad sg{lse, entropy, g_logp, g_entropy, logit_scale};
-  const void* hd = h;
-  if (targets) {
-    if (cudaError_t e = launch_mask_rows(h, targets, p->T, pd.V_real, p->ignore_index, p->H * esize_of(*p), hm,
-                                         status, st))
-      return cuda_status(e);
-    hd = hm;
-  }
+  float* P = L.parts > 1 ? reinterpret_cast<float*>(front + L.P) : nullptr;
+  // The fp32 dH: the caller's, or the sum of a bf16 one.
+  float* dH = dH_bf16 ? reinterpret_cast<float*>(front + L.acc) : static_cast<float*>(dH_out);
+  ScoreBwd sb{sg, targets ? front + L.hm : nullptr, P, dW_dtype == VCE_BF16};
   if (!p->tied_weights && p->Vp > p->V_real) {
     if (cudaError_t me = cudaMemsetAsync(static_cast<char*>(dW) + row_bytes * p->V_real, 0,
                                          row_bytes * (p->Vp - p->V_real), st))
       return cuda_status(me);
   }
   const bool acc_out = (p->flags & VCE_FLAG_ACCUMULATE_DH) != 0;
-  const bool acc_dh = acc_out && acc_bytes == 0;   // a bf16 dH is added in the rounding step
+  const int64_t n = p->T * p->H;
   for (int64_t c0 = 0; c0 < p->V_real; c0 += vc) {
     const int vc_act = static_cast<int>((p->V_real - c0) < vc ? (p->V_real - c0) : vc);
+    const bool last = c0 + vc >= p->V_real;
+    const bool add = c0 > 0 || (acc_out && !dH_bf16);   // a bf16 dH is added in the rounding step
+    int parts = 1;
     cudaError_t e;
-    if (p->dtype == VCE_BF16) {
-      const int parts = dh_flags ? tc_dh_parts(*p, vc_act) : 1;
-      e = launch_tc_bwd_chunk(*p, hd, W, targets, lse, 0.0f, static_cast<int>(c0), vc_act, G, static_cast<int>(vc), dH,
-                              c0 > 0 || acc_dh, dW, p->tied_weights != 0, dh_flags, parts, status, st, &sg,
-                              dW_dtype == VCE_BF16);
+    if (bf16) {
+      if (P) {   // every part of this chunk's K blocks (64 columns) has at least one
+        const int64_t kb = ceil_div(vc_act, 64);
+        parts = static_cast<int>(ceil_div(kb, ceil_div(kb, L.parts)));
+        sb.P = parts > 1 ? P : nullptr;
+      } else if (dh_flags) {
+        parts = tc_dh_parts(*p, vc_act);
+      }
+      e = launch_tc_bwd_chunk(*p, h, W, targets, lse, 0.0f, static_cast<int>(c0), vc_act, G, static_cast<int>(vc), dH,
+                              add, dW, p->tied_weights != 0, dh_flags, parts, status, st, &sb);
     } else {
-      float* Gf = static_cast<float*>(G);
-      const float* hf = static_cast<const float*>(hd);
-      const float* Wf = static_cast<const float*>(W);
-      e = launch_simt_score_grad(pd, hf, Wf, targets, sg, static_cast<int>(c0), vc_act, Gf, st);
-      if (e == cudaSuccess)   // dH (+)= G W[c0:c0+vc_act]
-        e = launch_sgemm(pd.T, pd.H, vc_act, Gf, vc_act, 1, Wf + c0 * p->H, p->H, 1, dH, p->H,
-                         (c0 > 0 || acc_dh) ? 1 : 0, st);
-      if (e == cudaSuccess)   // dW[c0:c0+vc_act] (+)= G^T h
-        e = launch_sgemm(vc_act, pd.H, pd.T, Gf, 1, vc_act, hf, p->H, 1, static_cast<float*>(dW) + c0 * p->H, p->H,
-                         p->tied_weights ? 1 : 0, st);
+      if (P) parts = f32_dh_parts(p->T, p->H, vc_act) < L.parts ? f32_dh_parts(p->T, p->H, vc_act) : L.parts;
+      e = launch_f32_score_bwd(pd, static_cast<const float*>(h), static_cast<const float*>(W), targets, sg,
+                               static_cast<int>(c0), vc_act, static_cast<float*>(G), vc, P, parts, dH, add,
+                               static_cast<float*>(dW), p->tied_weights != 0, status, st);
+    }
+    if (e == cudaSuccess && P && parts > 1) {
+      if (dH_bf16 && last)
+        e = launch_join(P, L.part_elems, parts, c0 > 0 ? dH : nullptr, acc_out, dH_out, true, n, st);
+      else
+        e = launch_join(P, L.part_elems, parts, nullptr, add, dH, false, n, st);
     }
     if (e != cudaSuccess) return cuda_status(e);
+    if (dH_bf16 && last && !(P && parts > 1)) return cuda_status(launch_dh_to_bf16(dH, dH_out, n, acc_out, st));
   }
-  if (acc_bytes) return cuda_status(launch_dh_to_bf16(dH, dH_out, p->T * p->H, acc_out, st));
   return VCE_OK;
 }
 
