@@ -65,10 +65,11 @@ __device__ __forceinline__ void write_top(uint64_t key, int64_t at, float scale,
 
 // ---------------------------------------------------------------------------
 // The K largest of many distinct keys, by one block. All functions are called by
-// every thread of the block, which has at least kBoundLists threads.
+// every thread of the block, which has a multiple of kBoundLists threads, at most
+// 1024.
 // ---------------------------------------------------------------------------
 constexpr int kBoundLists = 64;   // lists whose largest keys give the bound (at least kMaxTop)
-constexpr int kCandidates = 1024;
+constexpr int kCandidates = 2048;   // at least the threads of a block, and the classes of 32 quads of groups
 
 struct TopShared {
   unsigned long long list[kBoundLists];
@@ -80,7 +81,6 @@ struct TopShared {
 };
 
 __device__ __forceinline__ void top_init(TopShared& s) {
-  if (threadIdx.x < kBoundLists) s.list[threadIdx.x] = 0;
   if (threadIdx.x < kMaxTop) s.best[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     s.bound = 0;
@@ -89,13 +89,17 @@ __device__ __forceinline__ void top_init(TopShared& s) {
   __syncthreads();
 }
 
-// After each thread has raised its list (thread i: list i mod 64) to a key that
-// some element of its own part reaches: the K-th largest of the lists, which K
-// elements reach, or 0 when fewer than K lists hold a key.
-__device__ __forceinline__ void top_raise(TopShared& s, uint64_t key) {
-  if (key) atomicMax(&s.list[threadIdx.x & (kBoundLists - 1)], static_cast<unsigned long long>(key));
-}
+// Each thread gives the largest key that some element of its own part reaches.
+__device__ __forceinline__ void top_raise(TopShared& s, uint64_t key) { s.cand[threadIdx.x] = key; }
+// List l is that of the threads l, l + 64, ...: the K-th largest of the lists,
+// which K elements reach, or 0 when fewer than K lists hold a key.
 __device__ __forceinline__ uint64_t top_bound(TopShared& s, int K) {
+  __syncthreads();
+  if (threadIdx.x < kBoundLists) {
+    uint64_t k = 0;
+    for (uint32_t i = threadIdx.x; i < blockDim.x; i += kBoundLists) k = s.cand[i] > k ? s.cand[i] : k;
+    s.list[threadIdx.x] = k;
+  }
   __syncthreads();
   if (threadIdx.x < kBoundLists) {
     const uint64_t k = s.list[threadIdx.x];
@@ -157,12 +161,18 @@ __device__ void top_scan(TopShared& s, uint32_t n, int K, KeyAt key_at) {
 // Joins the threads' statistics; every thread gets the same bits. `sh` has 32 entries.
 __device__ __forceinline__ ScoreStat block_join(ScoreStat a, ScoreStat* sh) {
   const int lane = static_cast<int>(threadIdx.x & 31), warps = static_cast<int>(blockDim.x >> 5);
+  // the largest maximum first, then every part under it: one exponential a part,
+  // and sums whose bits do not depend on the lane
   auto over_warp = [&] {
+    float M = a.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float d = a.m == -INFINITY ? 0.0f : a.m - M, c = expf(d);
+    a = ScoreStat{M, c * a.S, c * fmaf(d, a.S, a.U)};
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const ScoreStat b{__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.S, o),
-                        __shfl_xor_sync(0xffffffffu, a.U, o)};
-      a = (lane & o) == 0 ? score_stat_join(a, b) : score_stat_join(b, a);
+      a.S += __shfl_xor_sync(0xffffffffu, a.S, o);
+      a.U += __shfl_xor_sync(0xffffffffu, a.U, o);
     }
   };
   over_warp();

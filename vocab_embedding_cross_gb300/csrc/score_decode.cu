@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
       tma_prefetch_desc(&mapW16);
       tma_prefetch_desc(&mapH);
     }
+    const uint64_t once = l2_evict_first();   // W is read once: the logits and h are to stay in L2
     Ring<kW> w;
     Ring<kH> hr;
     bool ok = true;
@@ -228,10 +229,11 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
             for (int j = 0; j < panels; ++j) {
               const uint32_t sP = sW + static_cast<uint32_t>(j) * kPanelBytes;
               if (n == kSub)
-                tma_load_2d(sP, &mapW, &wfull[w.slot], k0 + j * kPanel, r0 + s0);
+                tma_load_2d(sP, &mapW, &wfull[w.slot], k0 + j * kPanel, r0 + s0, once);
               else
                 for (int r = 0; r < n; r += 16)
-                  tma_load_2d(sP + static_cast<uint32_t>(r) * 128u, &mapW16, &wfull[w.slot], k0 + j * kPanel, r0 + s0 + r);
+                  tma_load_2d(sP + static_cast<uint32_t>(r) * 128u, &mapW16, &wfull[w.slot], k0 + j * kPanel,
+                              r0 + s0 + r, once);
             }
           }
           w.next();
