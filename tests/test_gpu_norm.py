@@ -182,3 +182,37 @@ def test_same_bits_each_time_and_in_a_graph():
         torch.cuda.synchronize()
         for a, b_ in zip(every, want):
             assert torch.equal(a.view(torch.uint8), b_.view(torch.uint8))
+
+
+def test_rows_past_32_bit_offsets():
+    """x of more than 2^31 elements: the last rows, and the sums over all of them."""
+    T, H = 1050001, 2048
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+    base = torch.randn((1, H), generator=g, device="cuda").bfloat16()
+    x.copy_(base.expand(T, H))
+    x[-3:] = torch.randn((3, H), generator=g, device="cuda").bfloat16()
+    p = problem("bf16", T, H, "bf16")
+    y = torch.empty_like(x)
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    vce.vce_norm_fwd(p, x, None, None, y, mean, rstd)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 2), slice(T - 3, T)):
+        xs = D.to_host_bits(x[rows])
+        yo, mu, r = S.norm_forward(xs)
+        assert np.all(np.abs(y[rows].float().cpu().numpy() - yo) <= 2.0 ** -8 * np.abs(yo) + 1e-4)
+        assert np.all(np.abs(rstd[rows].cpu().numpy() - r) <= 1e-4 * r)
+    assert bool((rstd[:-3] == rstd[0]).all())
+    dy = x                                        # any bf16 gradient
+    dw, db = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    vce.vce_norm_bwd(p, x, None, dy, mean, rstd, y, dw, db, D.workspace(vce.vce_workspace_size(p, vce.VCE_OP_NORM_BWD)))
+    torch.cuda.synchronize()
+    _, dw1, db1 = S.norm_backward(D.to_host_bits(x[:1]), None, D.to_host_bits(x[:1]), mean[:1].cpu().numpy(),
+                                  rstd[:1].cpu().numpy())
+    _, dw3, db3 = S.norm_backward(D.to_host_bits(x[-3:]), None, D.to_host_bits(x[-3:]), mean[-3:].cpu().numpy(),
+                                  rstd[-3:].cpu().numpy())
+    n = T - 3
+    # equal terms added one by one in chains of at most T / 152 rows: n u of the sum, u = 2^-24
+    for got, one, three in ((dw, dw1, dw3), (db, db1, db3)):
+        want = n * one + three
+        assert np.all(np.abs(got.cpu().numpy() - want) <= (T / 152 + 200) * U24 * n * (np.abs(one) + 0.01))

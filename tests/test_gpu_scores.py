@@ -458,3 +458,52 @@ def test_empty_batch():
     vce.vce_logprob_bwd(p, e, W, i, z, z, z, z, torch.empty((0, 64), device="cuda"), dW, D.workspace(256))
     torch.cuda.synchronize()
     assert not dW.any().item()
+
+
+@pytest.mark.parametrize("T", [1100])
+def test_gradient_with_parts_added_in_turn(T):
+    """Enough tiles of dH that its K parts are added one after the other."""
+    H, V = 1024, 4100
+    h, W, y, Vp = grid_case(T, H, V, "bf16", seed=24)
+    rng = np.random.default_rng(25)
+    gl, ge = (rng.standard_normal(T).astype(np.float32).astype(np.float64) * s for s in (1.0, 0.25))
+    ref = S.token_scores(h, W, y, V, 1.0)
+    got = run_bwd("bf16", h, W, y, V, Vp, ref, gl, ge, 1.0, flags=vce.VCE_FLAG_DH_BF16, dw_bf16=True)
+    check_bwd("bf16", got, h, W, y, V, ref, gl, ge, 1.0, dh_bf16=True, dw_bf16=True)
+    again = run_bwd("bf16", h, W, y, V, Vp, ref, gl, ge, 1.0, flags=vce.VCE_FLAG_DH_BF16, dw_bf16=True)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_tokens_in_several_passes():
+    """More tokens than one pass of the workspace takes, the last pass a short one."""
+    T, H, V, K = 50100, 64, 20000, 32
+    h, W, y, Vp = grid_case(T, H, V, "bf16", seed=26)
+    assert vce.vce_logprob_workspace_size(problem("bf16", T, H, Vp, V), K) < 600 << 20
+    got = run_fwd("bf16", h, W, y, V, Vp, K, 1.0)
+    rng = np.random.default_rng(27)
+    rows = np.unique(np.concatenate([rng.integers(0, T, 200), np.arange(T - 150, T), np.arange(0, T, 2048)]))
+    ref = S.token_scores(h[rows], W, y[rows], V, 1.0, K)
+    check_fwd({k: v[rows] for k, v in got.items()}, ref, 1.0, K)
+    assert np.all(np.isfinite(got["lse"])) and np.all((got["top_ids"] >= 0) & (got["top_ids"] < V))
+
+
+def test_classes_past_32_bit_offsets():
+    """W of more than 2^31 elements: the classes that matter lie at its end."""
+    H, V = 2048, 1100032
+    W = torch.zeros((V, H), dtype=torch.bfloat16, device="cuda")
+    last = torch.arange(V - 40, V, device="cuda")
+    W[last, 0] = (torch.arange(40, device="cuda") + 1).bfloat16()
+    for T in (3, 200):
+        h = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+        h[:, 0] = 0.5
+        y = torch.full((T,), V - 1, dtype=torch.int64, device="cuda")
+        p = vce.problem(T, H, V, V, 8, vce.VCE_BF16)
+        logp, ent, lse = (torch.empty(T, device="cuda") for _ in range(3))
+        ids, tl = torch.empty((T, 20), dtype=torch.int64, device="cuda"), torch.empty((T, 20), device="cuda")
+        vce.vce_logprob_fwd(p, h, W, y, logp, ent, lse, ids, tl, ws=D.workspace(vce.vce_logprob_workspace_size(p, 20)))
+        torch.cuda.synchronize()
+        z = 0.5 * (np.arange(40) + 1)
+        want = np.log(np.exp(z).sum() + V - 40)
+        assert np.abs(lse.cpu().numpy() - want).max() < 1e-3
+        assert np.abs(logp.cpu().numpy() - (z[-1] - want)).max() < 1e-3
+        assert torch.equal(ids, torch.arange(V - 1, V - 21, -1, device="cuda").expand(T, 20))
