@@ -827,15 +827,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (y >= vc0 && y < vc0 + nval) a.ztgt[t] = select32(x, static_cast<int>(y - vc0));
           // maxima of eight columns each, then of the chunk
           float gm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto xf = [&](int j) { return __uint_as_float(x[j]); };
           if (nval == 32) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) gm[j >> 3] = fmaxf(gm[j >> 3], __uint_as_float(x[j]));
+            for (int g = 0; g < 4; ++g) {
+              const int j = 8 * g;
+              gm[g] = max3(max3(xf(j), xf(j + 1), xf(j + 2)), max3(xf(j + 3), xf(j + 4), xf(j + 5)),
+                           fmaxf(xf(j + 6), xf(j + 7)));
+            }
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (j < nval) gm[j >> 3] = fmaxf(gm[j >> 3], __uint_as_float(x[j]));
           }
-          const float cm = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
+          // (a group of NaN alone gives NaN: taken as the least)
+          const float cm = fmaxf(max3(gm[0], gm[1], gm[2]), fmaxf(gm[3], -INFINITY));
           if (cm > m_run) {
             const float d = m_run == -INFINITY ? 0.0f : (m_run - cm) * sL;   // nothing summed yet: 0 or NaN
             const float c = ex2_approx(d);
@@ -844,23 +850,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             m_run = cm;
           }
           const float mL = m_run == -INFINITY ? 0.0f : m_run * sL;
-          float s0 = 0.0f, s1 = 0.0f, u0 = 0.0f, u1 = 0.0f;
-          // exp(-inf) * -inf is kept out by the clamp: 2^-300 is 0
-          if (nval == 32) {
+          float s0, s1, u0, u1;
+          if (nval == 32) {   // two columns an instruction, two chains a sum
+            uint64_t sa = 0, sb = 0, ua = 0, ub = 0;   // pairs of +0
+            const uint64_t sL2 = pack_f32x2(sL, sL), mL2 = pack_f32x2(-mL, -mL);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float d0 = fmaf(__uint_as_float(x[j]), sL, -mL), d1 = fmaf(__uint_as_float(x[j + 1]), sL, -mL);
-              const float e0 = ex2_approx(d0), e1 = ex2_approx(d1);
-              s0 += e0;
-              s1 += e1;
-              u0 = fmaf(e0, fmaxf(d0, -300.0f), u0);
-              u1 = fmaf(e1, fmaxf(d1, -300.0f), u1);
+            for (int j = 0; j < 32; j += 4) {
+              const uint64_t da = fma_f32x2(pack_f32x2(xf(j), xf(j + 1)), sL2, mL2);
+              const uint64_t db = fma_f32x2(pack_f32x2(xf(j + 2), xf(j + 3)), sL2, mL2);
+              float d0, d1, d2, d3;
+              unpack_f32x2(da, d0, d1);
+              unpack_f32x2(db, d2, d3);
+              const uint64_t ea = pack_f32x2(ex2_approx(d0), ex2_approx(d1));
+              const uint64_t eb = pack_f32x2(ex2_approx(d2), ex2_approx(d3));
+              sa = add_f32x2(sa, ea);
+              sb = add_f32x2(sb, eb);
+              ua = fma_f32x2(ea, da, ua);
+              ub = fma_f32x2(eb, db, ub);
             }
-          } else {
+            unpack_f32x2(add_f32x2(sa, sb), s0, s1);
+            unpack_f32x2(add_f32x2(ua, ub), u0, u1);
+          }
+          if (nval != 32 || u0 + u1 != u0 + u1) {
+            // A ragged chunk, or exp(-inf) * -inf (or a NaN logit) in U: column by
+            // column with the exponent clamped in U's product, where 2^-300 is 0.
+            s0 = s1 = u0 = u1 = 0.0f;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (j < nval) {
-                const float d0 = fmaf(__uint_as_float(x[j]), sL, -mL);
+                const float d0 = fmaf(xf(j), sL, -mL);
                 const float e0 = ex2_approx(d0);
                 s0 += e0;
                 u0 = fmaf(e0, fmaxf(d0, -300.0f), u0);
