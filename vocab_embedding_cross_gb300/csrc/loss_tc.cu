@@ -396,9 +396,9 @@ __device__ __noinline__ int sift_list(uint2* list, int n, float bound) {
   return kept;
 }
 
-// A value that at least K of the row's slots reach, near their K-th largest
-// (the last 1/4096 of their range is not worth more steps); 0 while fewer than
-// K slots hold one.
+// A value that at least K of the row's slots reach, near their K-th largest (K
+// exactly, or within 1/4096 of their range: more steps would gain nothing); 0 while
+// fewer than K slots hold one.
 __device__ __noinline__ uint32_t slot_bound(const uint32_t* slots, int K) {
   uint32_t v[kSlots], lo = 0xFFFFFFFFu, hi = 0;
   int filled = 0;
@@ -414,15 +414,106 @@ __device__ __noinline__ uint32_t slot_bound(const uint32_t* slots, int K) {
 #pragma unroll 1
   for (int step = 0; step < 12 && lo < hi; ++step) {
     const uint32_t mid = lo + ((hi - lo) >> 1) + 1;
-    int c = 0;
+    int c[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i) c += v[i] >= mid ? 1 : 0;
-    if (c >= K)
+    for (int i = 0; i < kSlots; ++i) c[i & 3] += v[i] >= mid ? 1 : 0;
+    const int n = (c[0] + c[1]) + (c[2] + c[3]);
+    if (n >= K)
       lo = mid;
     else
       hi = mid - 1;
+    if (n == K) break;
   }
   return lo;
+}
+
+// Counts the eight-column groups of a tile half (128 accumulator columns from ta,
+// the first `ncols` of them real) into the row's slots, from slot `slot` on.
+__device__ __noinline__ void count_groups(uint32_t ta, int ncols, uint32_t* slots, int slot) {
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[32];
+    tmem_ld_32x32b_x32(ta + 32 * c, x);
+    tmem_ld_wait();
+    reg_fence(x);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 8 * g; j < 8 * g + 8; ++j)
+        if (32 * c + j < ncols) m = fmaxf(m, __uint_as_float(x[j]));
+      if (slots && 32 * c + 8 * g < ncols)
+        atomicMax(slots + 32 * ((slot + 4 * c + g) & (kSlots - 1)), ordered_bits(m));
+    }
+  }
+}
+
+// A row's list while its unit is worked on. `thr` is what an entry has to reach,
+// `bound` the row's bound as last read (-inf before the first).
+struct RowList {
+  uint2* base;             // the warp's lists
+  uint32_t* slots;         // of the row, or null (no such token)
+  const uint32_t* word;    // the row's bound in global memory, or null
+  int K, n;
+  float thr, bound;
+};
+__device__ __forceinline__ void take_bound(RowList& r, uint32_t o) {
+  if (o) r.bound = ordered_value(o);
+  r.thr = fmaxf(r.thr, r.bound);
+}
+// Lists longer than `most` (K + kListSlack or more) drop what the bound has
+// overtaken and, where that is not enough and they must, are cut.
+__device__ __forceinline__ void shorten(RowList& r, int most, bool must) {
+  if (!__any_sync(0xffffffffu, r.n > most)) return;
+  take_bound(r, r.word ? __ldcg(r.word) : 0);
+  if (r.n > most) r.n = sift_list(r.base + (threadIdx.x & 31), r.n, r.bound);
+  if (!must || !__any_sync(0xffffffffu, r.n > most)) return;
+  const float2 v = cut_lists(r.base, r.K, r.n > most, r.n, r.thr);
+  r.n = __float_as_int(v.x);
+  r.thr = v.y;
+}
+
+// Appends what reaches r.thr in the groups of `any` (bit 4 c + g: columns 32 c + 8 g
+// on), read from the accumulator again. `mine`: the groups in which this row has a
+// hit; their chunks are counted into the slots unless the tile has been already.
+// Returns (n as bits, thr).
+__device__ __noinline__ float2 append_hits(uint32_t ta, uint32_t col0, int ncols, unsigned any, unsigned mine,
+                                           bool count, int slot, RowList r) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const unsigned groups = (any >> (4 * c)) & 15u;
+    if (groups == 0) continue;
+    uint32_t x[32];
+    tmem_ld_32x32b_x32(ta + 32 * c, x);
+    tmem_ld_wait();
+    reg_fence(x);
+    if (32 * c + 32 > ncols) {   // columns past the last class reach nothing
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (32 * c + j >= ncols) x[j] = 0x7FC00000u;
+    }
+    if (count && ((mine >> (4 * c)) & 15u)) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) m = fmaxf(m, __uint_as_float(x[j]));
+      atomicMax(r.slots + 32 * ((slot + c) & (kSlots - 1)), ordered_bits(m));
+    }
+    shorten(r, kListCap - 32, true);
+    uint2* to = r.base + r.n * 32 + lane;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      if ((groups & (1u << g)) == 0) continue;
+#pragma unroll
+      for (int j = 8 * g; j < 8 * g + 8; ++j)
+        if (__uint_as_float(x[j]) >= r.thr) {
+          *to = make_uint2(x[j], col0 + static_cast<uint32_t>(32 * c + j));
+          to += 32;
+        }
+    }
+    r.n = static_cast<int>(to - r.base) >> 5;
+  }
+  return make_float2(__int_as_float(r.n), r.thr);
 }
 
 template <int MODE>
@@ -787,43 +878,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int K = a.sl.K;
         const float sL = a.sl.scale * kLog2e;
         float m_run = -INFINITY, s_run = 0.0f, u_run = 0.0f;   // of the unscaled maximum; sums in base 2
-        float thr = row_ok && K ? -INFINITY : INFINITY;
-        int n = 0;
-        uint2* list = K ? a.sl.scratch + static_cast<int64_t>(blockIdx.x * kEpiWarps + e) * (kListCap * 32) : nullptr;
-        // the row's slots, [T/32][kSlots][32], and bound
-        uint32_t* slots = K ? a.sl.slots + (static_cast<int64_t>(t >> 5) * (kSlots * 32) + (t & 31)) : nullptr;
         const bool listed = row_ok && K;
-        float bound = -INFINITY;
+        RowList rl{};
+        rl.K = K;
+        rl.thr = listed ? -INFINITY : INFINITY;
+        rl.bound = -INFINITY;
+        if (K) rl.base = a.sl.scratch + static_cast<int64_t>(blockIdx.x * kEpiWarps + e) * (kListCap * 32);
+        if (listed) {
+          rl.slots = a.sl.slots + (static_cast<int64_t>(t >> 5) * (kSlots * 32) + (t & 31));   // [T/32][kSlots][32]
+          rl.word = a.sl.bound + t;
+        }
         // The bound is read at a tile's start for the next one, so that no warp waits for L2.
-        uint32_t next_bound = listed ? __ldcg(a.sl.bound + t) : 0;
-        auto take_bound = [&](uint32_t o) {
-          if (o) bound = ordered_value(o);
-          thr = fmaxf(thr, bound);
-        };
-        auto refresh = [&] { take_bound(listed ? __ldcg(a.sl.bound + t) : 0); };
+        uint32_t next_bound = listed ? __ldcg(rl.word) : 0;
         // Units come in ascending order; the bound moves as 1 / (classes seen), so
         // units 0, 1, 2, 3, 4, 6, 8, 12, 16, 24, ... work it out anew.
         const int below_top = u & (u - 1);
         const bool raises = half == 0 && (below_top & (below_top - 1)) == 0;
         auto raise_bound = [&] {
-          if (const uint32_t o = listed ? slot_bound(slots, K) : 0) atomicMax(a.sl.bound + t, o);
+          if (const uint32_t o = listed ? slot_bound(rl.slots, K) : 0) atomicMax(a.sl.bound + t, o);
         };
-        // Lists longer than `most` (K + kListSlack or more) are shortened to at most that.
-        auto shorten = [&](int most, bool must) {
-          if (!__any_sync(0xffffffffu, n > most)) return;
-          refresh();
-          if (n > most) n = sift_list(list + lane, n, bound);
-          if (!must || !__any_sync(0xffffffffu, n > most)) return;
-          const float2 v = cut_lists(list, K, n > most, n, thr);
-          n = __float_as_int(v.x);
-          thr = v.y;
-        };
-        int slot = 0;           // of the next chunk
-        bool counted = false;   // this tile's columns are in the slots already
+        unsigned hits = 0;   // groups of the tile half in which the row reaches its threshold
         auto chunk = [&](const uint32_t (&x)[32], int64_t vc0) {
           const int64_t nval64 = us.vlim - vc0;
           const int nval = nval64 >= 32 ? 32 : (nval64 <= 0 ? 0 : static_cast<int>(nval64));
-          if (nval == 0) return;
+          if (nval == 0) {
+            hits >>= 4;
+            return;
+          }
           if (y >= vc0 && y < vc0 + nval) a.ztgt[t] = select32(x, static_cast<int>(y - vc0));
           // maxima of eight columns each, then of the chunk
           float gm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -886,27 +967,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           s_run += s0 + s1;
           u_run += u0 + u1;
-          if (!K) return;
-          const bool hit = cm >= thr;
-          if (hit && !counted) atomicMax(slots + 32 * slot, ordered_bits(cm));
-          slot = (slot + 1) & (kSlots - 1);
-          if (__any_sync(0xffffffffu, hit)) {
-            shorten(kListCap - 32, true);
-            uint32_t at = static_cast<uint32_t>(n * 32 + lane) * 8u;
-            char* const to = reinterpret_cast<char*>(list);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              if (!__any_sync(0xffffffffu, gm[g] >= thr)) continue;
-#pragma unroll
-              for (int j = 8 * g; j < 8 * g + 8; ++j) {
-                if (__uint_as_float(x[j]) >= thr && j < nval) {
-                  *reinterpret_cast<uint2*>(to + at) = make_uint2(x[j], static_cast<uint32_t>(vc0) + j);
-                  at += 32 * 8;
-                }
-              }
-            }
-            n = static_cast<int>(at >> 8);
-          }
+          hits = (hits >> 4) | (gm[0] >= rl.thr ? 0x1000u : 0u) | (gm[1] >= rl.thr ? 0x2000u : 0u) |
+                 (gm[2] >= rl.thr ? 0x4000u : 0u) | (gm[3] >= rl.thr ? 0x8000u : 0u);
         };
         for (int tt = 0; tt < us.ntiles; ++tt) {
           const uint32_t acc = tile_count & 1u;
@@ -915,40 +977,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          take_bound(next_bound);
-          if (listed) next_bound = __ldcg(a.sl.bound + t);
+          take_bound(rl, next_bound);
+          if (listed) next_bound = __ldcg(rl.word);
           const int64_t vc = us.vb + static_cast<int64_t>(tt) * BN + half * 128;
+          const int ncols = us.vlim - vc >= 128 ? 128 : (us.vlim > vc ? static_cast<int>(us.vlim - vc) : 0);
           const uint32_t ta = lane_base + acc * BN;
-          uint32_t xa[32], xb[32];
-          counted = false;
-          if (__any_sync(0xffffffffu, listed && bound == -INFINITY)) {
-            counted = tt == 0;
-            if (counted) {
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                tmem_ld_32x32b_x32(ta + 32 * c, xa);
-                tmem_ld_wait();
-                reg_fence(xa);
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                  float gm = -INFINITY;
-#pragma unroll
-                  for (int j = 8 * g; j < 8 * g + 8; ++j)
-                    if (vc + 32 * c + j < us.vlim) gm = fmaxf(gm, __uint_as_float(xa[j]));
-                  if (listed && vc + 32 * c + 8 * g < us.vlim)
-                    atomicMax(slots + 32 * ((u * 32 + half * 16 + c * 4 + g) & (kSlots - 1)), ordered_bits(gm));
-                }
-              }
+          bool count = true;
+          if (__any_sync(0xffffffffu, listed && rl.bound == -INFINITY)) {
+            if (tt == 0) {
+              count_groups(ta, ncols, rl.slots, u * 32 + half * 16);
+              count = false;
             }
             raise_bound();
-            refresh();
+            take_bound(rl, listed ? __ldcg(rl.word) : 0);
           } else if (raises && tt == (us.ntiles >> 1)) {
             raise_bound();
           }
-          if (K) {
-            shorten(K + kListSlack, false);
-            slot = ((u * (a.ug.uw / BN) + tt) * 8 + half * 4) & (kSlots - 1);
-          }
+          uint32_t xa[32], xb[32];
+          hits = 0;
           tmem_ld_32x32b_x32(ta, xa);
           tmem_ld_wait();
           reg_fence(xa);
@@ -958,25 +1004,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             chunk(xa, vc + 64 * c);
             tmem_ld_wait();
             reg_fence(xb);
-            if (c == 0) {
-              tmem_ld_32x32b_x32(ta + 64, xa);
-            } else {
-              release(acc);
-            }
+            if (c == 0) tmem_ld_32x32b_x32(ta + 64, xa);
             chunk(xb, vc + 64 * c + 32);
             tmem_ld_wait();
             reg_fence(xa);
           }
+          if (!listed) hits = 0;   // an infinite logit reaches any threshold
+          if (const unsigned any = __reduce_or_sync(0xffffffffu, hits)) {
+            const float2 v = append_hits(ta, static_cast<uint32_t>(vc), ncols, any, hits, count,
+                                         (u * (a.ug.uw / BN) + tt) * 8 + half * 4, rl);
+            rl.n = __float_as_int(v.x);
+            rl.thr = v.y;
+          }
+          release(acc);
+          if (K) shorten(rl, K + kListSlack, false);
           ++tile_count;
         }
         if (!ok) break;
         if (K) {   // the unit's entries to the row's list
-          shorten(K + kListSlack, true);
+          shorten(rl, K + kListSlack, true);
+          const int n = listed ? rl.n : 0;
           if (n > 0) {
             uint2* to = a.sl.row_list + static_cast<int64_t>(t) * a.sl.row_cap + atomicAdd(a.sl.row_count + t, n);
-            for (int i = 0; i < n; ++i) {
-              const uint2 v = list[i * 32 + lane];
-              to[i] = make_uint2(ordered_bits(__uint_as_float(v.x)), 0xFFFFFFFFu - v.y);
+            for (int i = 0; i < n; i += 8) {   // eight loads in flight
+              uint2 v[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (i + j < n) v[j] = rl.base[(i + j) * 32 + lane];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (i + j < n) to[i + j] = make_uint2(ordered_bits(__uint_as_float(v[j].x)), 0xFFFFFFFFu - v[j].y);
             }
           }
           __syncwarp();
