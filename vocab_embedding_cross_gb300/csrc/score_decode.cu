@@ -387,9 +387,9 @@ constexpr int kMergeThreads = 1024;
 constexpr int kMergePick = 512;    // groups read for candidates
 constexpr int kMergeKeep = 3;      // quadruples of group maxima that each thread keeps in registers
 
-// One block per token. A group of 16 classes with maximum g holds a key of at
-// least (g, its last class), so the K-th largest such key over 64 disjoint
-// lists' best groups bounds the K-th largest key of the row from below; only
+// One block per token. Four neighbouring groups of 16 classes with maximum g hold a
+// key of at least (g, their last class), so the K-th largest such key over 64
+// disjoint lists' best ones bounds the K-th largest key of the row from below; only
 // groups that reach (g, first class) >= the bound are read, one half-warp each.
 // Equal logits do not widen the choice: an all-equal row reads about the first
 // K groups.
@@ -418,32 +418,37 @@ __global__ void __launch_bounds__(kMergeThreads)
   // Thread i reads group quadruples i, i + 1024, ...; the first kMergeKeep stay in registers.
   const uint4* gm = K ? reinterpret_cast<const uint4*>(gmax + t * ldg) : nullptr;
   const int quads = K ? (groups + 3) >> 2 : 0;
-  auto low_key = [&](uint32_t g, int i) -> uint64_t {   // 0 for a group of NaN alone, and past the last group
-    if (!g || i >= groups) return 0;
-    return (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(min(16 * i + 16, V) - 1));
+  // A thread's best quadruple is found by its maxima alone, 32 bits; its key is that
+  // of the quadruple's last class, which some class of it reaches.
+  uint32_t most = 0;   // 0: groups of NaN alone, and words past the last group
+  int most_at = 0;
+  auto words = [&](int quad) {
+    uint4 g = gm[quad];
+    if (4 * quad + 4 > groups) {   // the row is padded to a multiple of four words
+      if (4 * quad + 1 >= groups) g.y = 0;
+      if (4 * quad + 2 >= groups) g.z = 0;
+      g.w = 0;
+    }
+    return g;
   };
-  auto high_key = [&](uint32_t g, int i) -> uint64_t {
-    if (!g || i >= groups) return 0;
-    return (static_cast<uint64_t>(g) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(16 * i));
-  };
-  uint64_t kmax = 0;
   auto raise = [&](const uint4& g, int quad) {
-    const uint32_t w[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t k = low_key(w[j], 4 * quad + j);
-      kmax = k > kmax ? k : kmax;
+    const uint32_t m = max(max(g.x, g.y), max(g.z, g.w));
+    if (m > most) {
+      most = m;
+      most_at = quad;
     }
   };
   uint4 keep[kMergeKeep];
 #pragma unroll
   for (int c = 0; c < kMergeKeep; ++c) {
     const int quad = tid + c * kMergeThreads;
-    keep[c] = quad < quads ? gm[quad] : make_uint4(0, 0, 0, 0);
+    keep[c] = quad < quads ? words(quad) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int c = 0; c < kMergeKeep; ++c) raise(keep[c], tid + c * kMergeThreads);
-  for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) raise(gm[quad], quad);
+  for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) raise(words(quad), quad);
+  const uint64_t kmax =
+      most ? (static_cast<uint64_t>(most) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(min(64 * most_at + 64, V) - 1)) : 0;
   if (K) top_raise(top, kmax);
   a = block_join(a, sh);
   const float l = score_lse(a);
@@ -452,12 +457,15 @@ __global__ void __launch_bounds__(kMergeThreads)
   if (K == 0) return;
   const uint64_t bound = top_bound(top, K);
   const float* z = Z + t * ldz;
+  const uint32_t bound_hi = static_cast<uint32_t>(bound >> 32);
   auto choose = [&](const uint4& g, int quad) {
+    if (max(max(g.x, g.y), max(g.z, g.w)) < bound_hi) return;
     const uint32_t w[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint64_t k = high_key(w[j], 4 * quad + j);
-      if (k != 0 && k >= bound) {
+      // the key that the group's first class would have with the group's maximum
+      const uint64_t k = (static_cast<uint64_t>(w[j]) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(64 * quad + 16 * j));
+      if (w[j] != 0 && k >= bound) {
         const int at = atomicAdd(&s_pick, 1);
         if (at < kMergePick) pick[at] = 4 * quad + j;
       }
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   };
 #pragma unroll
   for (int c = 0; c < kMergeKeep; ++c) choose(keep[c], tid + c * kMergeThreads);
-  for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) choose(gm[quad], quad);
+  for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) choose(words(quad), quad);
   __syncthreads();
   const int n_pick = s_pick;
   if (n_pick <= kMergePick)
