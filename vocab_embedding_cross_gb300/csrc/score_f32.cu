@@ -5,13 +5,13 @@
 //   GRAD    G  = score gradient of (h W^T)
 //   DH      dH = G W      (K, the classes, cut into parts where dH has few tiles)
 //   DW      dW = G^T h    (rows of h without a real target read as zero)
-// A block computes a 64 x 64 tile, 4 x 4 a thread, over slices of 16 along K; the
+// A block computes a 64 x 64 tile, 4 x 4 a thread, over slices of 32 along K; the
 // next slice is fetched into registers while the current one is multiplied out of
 // one of two shared-memory buffers. Small heads are bound by latency, so the
 // parts of DH matter more than the inner loop: one 64 x 64 tile over K = 1000 as
 // one block took 61 us.
 //
-// The parts are joined, in part order, by join_kernel, which also serves the
+// The parts are joined, in a fixed order, by join_kernel, which also serves the
 // tensor-core path's dH.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -24,7 +24,7 @@
 namespace vce {
 namespace {
 
-constexpr int kTile = 64, kSlice = 16;
+constexpr int kTile = 64, kSlice = 32;
 enum Form : int { LOGITS, GRAD, DH, DW };
 
 struct F32Args {
@@ -64,37 +64,45 @@ __global__ void __launch_bounds__(256) f32_product_kernel(const F32Args a) {
   const int n0 = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.m_tiles)) * kTile;
   const int kb = static_cast<int>(blockIdx.z) * a.k_part;
   const int ke = kb + a.k_part < a.K ? kb + a.k_part : a.K;
-  // Along K: row tid / 4, four K from 4 (tid % 4). Along M or N: K row tid / 16, four columns from 4 (tid % 16).
-  const int kr = tid >> 2, kc = (tid & 3) * 4, cr = tid >> 4, cc = (tid & 15) * 4;
-  float4 fa, fb;
+  // Two quadruples of each operand a thread. Along K: rows tid / 8 and 32 on, four K
+  // from 4 (tid % 8). Along M or N: K rows tid / 16 and 16 on, four columns from 4 (tid % 16).
+  const int kr = tid >> 3, kc = (tid & 7) * 4, cr = tid >> 4, cc = (tid & 15) * 4;
+  float4 fa[2], fb[2];
   auto fetch = [&](int k0) {
-    if (kATrans)
-      fa = k0 + cr < ke ? row4(a.A + (k0 + cr) * a.lda + m0 + cc, a.M - m0 - cc) : make_float4(0, 0, 0, 0);
-    else
-      fa = m0 + kr < a.M ? row4(a.A + (m0 + kr) * a.lda + k0 + kc, ke - k0 - kc) : make_float4(0, 0, 0, 0);
-    if (kBTrans) {
-      fb = n0 + kr < a.N ? row4(a.B + (n0 + kr) * a.ldb + k0 + kc, ke - k0 - kc) : make_float4(0, 0, 0, 0);
-    } else {
-      bool take = k0 + cr < ke;
-      if (FORM == DW && take && a.targets) {   // a row of h takes part if its token does
-        const int64_t y = a.targets[k0 + cr];
-        take = y >= 0 && y < a.V;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = kr + 32 * q, k = k0 + cr + 16 * q;
+      if (kATrans)
+        fa[q] = k < ke ? row4(a.A + k * a.lda + m0 + cc, a.M - m0 - cc) : make_float4(0, 0, 0, 0);
+      else
+        fa[q] = m0 + r < a.M ? row4(a.A + (m0 + r) * a.lda + k0 + kc, ke - k0 - kc) : make_float4(0, 0, 0, 0);
+      if (kBTrans) {
+        fb[q] = n0 + r < a.N ? row4(a.B + (n0 + r) * a.ldb + k0 + kc, ke - k0 - kc) : make_float4(0, 0, 0, 0);
+      } else {
+        bool take = k < ke;
+        if (FORM == DW && take && a.targets) {   // a row of h takes part if its token does
+          const int64_t y = a.targets[k];
+          take = y >= 0 && y < a.V;
+        }
+        fb[q] = take ? row4(a.B + k * a.ldb + n0 + cc, a.N - n0 - cc) : make_float4(0, 0, 0, 0);
       }
-      fb = take ? row4(a.B + (k0 + cr) * a.ldb + n0 + cc, a.N - n0 - cc) : make_float4(0, 0, 0, 0);
     }
   };
   auto keep = [&](int buf) {
-    const float va[4] = {fa.x, fa.y, fa.z, fa.w}, vb[4] = {fb.x, fb.y, fb.z, fb.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (kATrans)
-        As[buf][cr][cc + j] = va[j];
-      else
-        As[buf][kc + j][kr] = va[j];
-      if (kBTrans)
-        Bs[buf][kc + j][kr] = vb[j];
-      else
-        Bs[buf][cr][cc + j] = vb[j];
+    for (int q = 0; q < 2; ++q) {
+      const float va[4] = {fa[q].x, fa[q].y, fa[q].z, fa[q].w}, vb[4] = {fb[q].x, fb[q].y, fb[q].z, fb[q].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (kATrans)
+          As[buf][cr + 16 * q][cc + j] = va[j];
+        else
+          As[buf][kc + j][kr + 32 * q] = va[j];
+        if (kBTrans)
+          Bs[buf][kc + j][kr + 32 * q] = vb[j];
+        else
+          Bs[buf][cr + 16 * q][cc + j] = vb[j];
+      }
     }
   };
   float acc[4][4] = {};
@@ -147,42 +155,63 @@ __global__ void __launch_bounds__(256) f32_product_kernel(const F32Args a) {
   }
 }
 
-// out[t, i] (+)= sum of the parts in part order (after `before`, where there is
-// one), rounded once. parts are P[part][part_rows][H] with part_rows >= T.
+// out[t, i] (+)= before + the sum of the parts, rounded once. A block takes 32
+// quadruples of columns with eight threads each, which add every eighth part; their
+// sums are added in order (one thread a quadruple took 13 us to add 76 parts).
+// parts are P[part][rows][H], rows >= T.
+constexpr int kJoinLanes = 8;
 template <typename O>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kJoinLanes)
     join_kernel(const float4* __restrict__ P, int64_t part4, int parts, const float4* __restrict__ before, int add,
                 O* __restrict__ out, int64_t n4) {
+  __shared__ float4 sh[kJoinLanes][32];
   grid_dep_launch();
   grid_dep_wait();
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < n4;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    float4 a = before ? before[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * 32; i0 < n4; i0 += static_cast<int64_t>(gridDim.x) * 32) {
+    const int64_t i = i0 + x;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < n4) {
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-      const float4 v = P[p * part4 + i];
-      a.x += v.x;
-      a.y += v.y;
-      a.z += v.z;
-      a.w += v.w;
-    }
-    if constexpr (sizeof(O) == 16) {
-      if (add) {
-        const float4 o = out[i];
-        a = make_float4(o.x + a.x, o.y + a.y, o.z + a.z, o.w + a.w);
+      for (int p = y; p < parts; p += kJoinLanes) {
+        const float4 v = P[p * part4 + i];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
       }
-      out[i] = a;
-    } else {
-      if (add) {
-        const uint2 o = out[i];
-        a.x += __uint_as_float(o.x << 16);
-        a.y += __uint_as_float(o.x & 0xFFFF0000u);
-        a.z += __uint_as_float(o.y << 16);
-        a.w += __uint_as_float(o.y & 0xFFFF0000u);
-      }
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
-      out[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
+    sh[y][x] = a;
+    __syncthreads();
+    if (y == 0 && i < n4) {
+#pragma unroll
+      for (int o = 1; o < kJoinLanes; ++o) {
+        const float4 v = sh[o][x];
+        a = make_float4(a.x + v.x, a.y + v.y, a.z + v.z, a.w + v.w);
+      }
+      if (before) {
+        const float4 v = before[i];
+        a = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+      }
+      if constexpr (sizeof(O) == 16) {
+        if (add) {
+          const float4 o = out[i];
+          a = make_float4(o.x + a.x, o.y + a.y, o.z + a.z, o.w + a.w);
+        }
+        out[i] = a;
+      } else {
+        if (add) {
+          const uint2 o = out[i];
+          a.x += __uint_as_float(o.x << 16);
+          a.y += __uint_as_float(o.x & 0xFFFF0000u);
+          a.z += __uint_as_float(o.y << 16);
+          a.w += __uint_as_float(o.y & 0xFFFF0000u);
+        }
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
+        out[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -200,11 +229,11 @@ cudaError_t launch_form(F32Args a, int parts, int kind, cudaStream_t st) {
 
 }  // namespace
 
-// One wave of two blocks an SM, a part being four slices at the least.
+// One wave of two blocks an SM, a part being two slices at the least.
 int f32_dh_parts(int64_t T, int64_t H, int64_t K) {
   const int64_t tiles = ceil_div(T, kTile) * ceil_div(H, kTile);
   int64_t parts = 2 * static_cast<int64_t>(current_device_info().num_sms) / (tiles > 0 ? tiles : 1);
-  const int64_t most = ceil_div(K, 4 * kSlice);
+  const int64_t most = ceil_div(K, 2 * kSlice);
   if (parts > most) parts = most;
   if (parts < 1) parts = 1;
   // no part empty
@@ -265,10 +294,10 @@ cudaError_t launch_f32_score_bwd(const ProbDev& pd, const float* h, const float*
 
 cudaError_t launch_join(const float* P, int64_t part_elems, int parts, const float* before, bool add, void* out,
                         bool out_bf16, int64_t n, cudaStream_t st) {
-  const int64_t n4 = n / 4, want = ceil_div(n4, 256), cap = static_cast<int64_t>(current_device_info().num_sms) * 8;
+  const int64_t n4 = n / 4, want = ceil_div(n4, 32), cap = static_cast<int64_t>(current_device_info().num_sms) * 8;
   const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
   auto go = [&](auto kern, auto* to) {
-    return launch_dependent(kern, grid, dim3(256), 0, st, reinterpret_cast<const float4*>(P), part_elems / 4, parts,
+    return launch_dependent(kern, grid, dim3(32 * kJoinLanes), 0, st, reinterpret_cast<const float4*>(P), part_elems / 4, parts,
                             reinterpret_cast<const float4*>(before), add ? 1 : 0, to, n4);
   };
   const cudaError_t e = out_bf16 ? go(join_kernel<uint2>, static_cast<uint2*>(out))
