@@ -114,6 +114,12 @@ def test_backward(T, H, dtype, dy, kind):
         assert np.all(np.abs(db.cpu().numpy() - want[2]) <= (T + 32) * U24 * da.sum(0))
 
 
+@pytest.mark.parametrize("T,H", [(1, 4), (37, 12), (300, 20), (200, 1028), (5, 8196)])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_backward_of_bf16_rows_that_are_not_whole_16_byte_units(T, H, kind):
+    test_backward(T, H, "f32", "bf16", kind)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_backward_accumulates_and_leaves_out_what_is_not_asked_for(dtype):
     T, H = 130, 264

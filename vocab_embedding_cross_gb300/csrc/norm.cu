@@ -499,8 +499,9 @@ __global__ void __launch_bounds__(512)
   *to = a;
 }
 
-// Rows too wide for registers (more than 4096 vectors forward, 1024 backward): one
-// block a row that reads it again from L2, and the column sums by a thread a column.
+// Rows too wide for registers (more than 4096 vectors forward, 1024 backward) or not
+// whole 16-byte units: one block a row that reads it again from L2, and the column
+// sums by a thread a column.
 __device__ __forceinline__ float load_f(const float* p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float load_f(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
 __device__ __forceinline__ void store_f(float* p, int64_t i, float v) { p[i] = v; }
@@ -597,11 +598,11 @@ struct Shape {
   size_t smem;
 };
 Shape shape(const vce_problem& p, int most, int cap_threads, int64_t slot_bytes, int64_t fixed_bytes,
-            int64_t min_smem) {   // min_smem: a group
+            int64_t min_smem, bool whole16) {   // min_smem: a group; whole16: every row is whole 16-byte units
   Shape s{};
   const int64_t nv = p.H / (p.dtype == VCE_BF16 ? 8 : 4);
   const int64_t sms = current_device_info().num_sms;
-  s.fused = nv <= static_cast<int64_t>(most) * cap_threads;
+  s.fused = whole16 && nv <= static_cast<int64_t>(most) * cap_threads;
   s.G = group_size(nv, most, cap_threads);
   int64_t groups = cap_threads / s.G;
   if (groups > kNamedBarriers && s.G > 32) groups = kNamedBarriers;
@@ -624,11 +625,13 @@ Shape shape(const vce_problem& p, int most, int cap_threads, int64_t slot_bytes,
 }
 Shape fwd_shape(const vce_problem& p) {
   const int64_t row = p.H * (p.dtype == VCE_BF16 ? 2 : 4);
-  return shape(p, 8, kFwdThreads, row, 2 * row, 0);
+  return shape(p, 8, kFwdThreads, row, 2 * row, 0, true);
 }
 Shape bwd_shape(const vce_problem& p) {
-  const int64_t row = p.H * ((p.dtype == VCE_BF16 ? 2 : 4) + ((p.flags & VCE_FLAG_DH_BF16) ? 2 : 4));
-  return shape(p, 4, kBwdThreads, row, 0, (2 * p.H + 64) * static_cast<int64_t>(sizeof(float)));
+  const int64_t d_row = p.H * ((p.flags & VCE_FLAG_DH_BF16) ? 2 : 4);
+  const int64_t row = p.H * (p.dtype == VCE_BF16 ? 2 : 4) + d_row;
+  // a bf16 dy beside an fp32 x with H = 4, 12, 20, ...: its rows cannot be copied in bulk
+  return shape(p, 4, kBwdThreads, row, 0, (2 * p.H + 64) * static_cast<int64_t>(sizeof(float)), d_row % 16 == 0);
 }
 
 // Raises the kernel's shared-memory limit once per device, then launches it.
