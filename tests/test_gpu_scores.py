@@ -328,6 +328,31 @@ def test_gradient(dtype, T, H, V, S_, scale, terms):
     assert not got[0][torch.from_numpy(y < 0).cuda()].any().item()
 
 
+@pytest.mark.parametrize("dtype,T", [("bf16", 7), ("bf16", 300), ("f32", 65)])
+@pytest.mark.parametrize("terms", ["logp", "entropy", "both"])
+def test_gradient_with_classes_of_minus_infinity(dtype, T, terms):
+    """Classes of logit -inf have no probability: no gradient of theirs, and none lost to the others."""
+    H, V, Vp = 64, 100, 128
+    h, W, y, _ = grid_case(T, H, V, dtype, seed=15, ignore=0.0)
+    W[3:90] = 0
+    W[3:90, 0] = np.uint16(0xFF80) if dtype == "bf16" else -np.inf
+    hf = S.as_f64(h)
+    hf[:, 0] = 1.0
+    h = store(hf, dtype)
+    y[:] = 95
+    real = np.r_[0:3, 90:V]
+    W13, y13 = W[real], np.full(T, 8)                     # the finite classes alone
+    rng = np.random.default_rng(16)
+    gl = rng.standard_normal(T).astype(np.float32).astype(np.float64) if terms != "entropy" else None
+    ge = rng.standard_normal(T).astype(np.float32).astype(np.float64) if terms != "logp" else None
+    ref = S.token_scores(h, W13, y13, 13, 1.0)
+    dH, dW = run_bwd(dtype, h, W, y, V, Vp, ref, gl, ge, 1.0)
+    assert not dW[3:90].any().item()
+    # column 0 of dH multiplies a zero of G by -inf, as the formula does
+    dH[:, 0] = torch.from_numpy(S.score_backward(h, W13, y13, 13, gl, ge, 1.0)[0][:, 0]).cuda()
+    check_bwd(dtype, (dH, dW[torch.from_numpy(real).cuda()]), h, W13, y13, 13, ref, gl, ge, 1.0)
+
+
 @pytest.mark.parametrize("minimal", [False, True])
 @pytest.mark.parametrize("T", [100, 600])
 def test_gradient_in_bf16(T, minimal):

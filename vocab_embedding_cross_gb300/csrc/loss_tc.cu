@@ -271,7 +271,8 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 //   dL/dz_v = s (g_logp ([v == y] - p_v) - g_entropy p_v (logp_v + entropy))
 //           = p_v (c0 + c1 (logp_v + entropy)) + [v == y] hit.
 // logp is one rounding of s z - lse before anything else is added, so that it
-// keeps its relative precision in peaked rows, where it is near 0.
+// keeps its relative precision in peaked rows, where it is near 0. The factor of p
+// is held above -200, where p is 0 in fp32, so that a logit of -inf gives 0.
 struct ScoreGradRow {
   float s, lse, ent, c0, c1, hit;
 };
@@ -289,7 +290,7 @@ __device__ __forceinline__ ScoreGradRow score_grad_row(const ScoreGrad& g, int t
 }
 __device__ __forceinline__ float score_grad(const ScoreGradRow& r, float z) {
   const float lp = fmaf(z, r.s, -r.lse);
-  return ex2_approx(lp * kLog2e) * fmaf(lp + r.ent, r.c1, r.c0);
+  return ex2_approx(lp * kLog2e) * fmaf(fmaxf(lp + r.ent, -200.0f), r.c1, r.c0);
 }
 
 // Lists of alternatives (SCORE). Every epilogue thread appends the logits of its

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(256) f32_product_kernel(const F32Args a) {
         const int n = n0 + 4 * tx + j;
         const float lp = fmaf(acc[i][j], a.sg.scale, -lse);
         const float p = expf(lp);
-        const float g = a.sg.scale * (gl * ((a.v0 + n == y ? 1.0f : 0.0f) - p) - ge * p * (lp + ent));
+        const float g = a.sg.scale * (gl * ((a.v0 + n == y ? 1.0f : 0.0f) - p) - ge * p * fmaxf(lp + ent, -200.0f));   // p is 0 below
         acc[i][j] = valid ? g : 0.0f;
       }
     }
