@@ -316,6 +316,12 @@ __device__ __forceinline__ float score_grad(const ScoreGradRow& r, float z) {
 // logits ascend with the class (one every 150 to 200 of them) and to the first
 // tiles. Thresholds only decide which losers are left out, so timing never
 // changes a result. At a unit's end the list's entries go to the row's own list.
+//
+// What bounds SCORE: the tensor cores, 2.65 ms for T = 8192, H = 2048, V = 151936
+// (1.92 PFLOP/s; 2.85 ms on data that costs the tensor pipe more power) where a tile's
+// 32 K blocks cover its epilogue; the epilogue below H = 1024 (H = 768, V = 50257: 368
+// us without alternatives and 510 with 20, where the product needs 338). Storing the
+// logits and selecting from them afterwards took 7.5 ms at the first size.
 constexpr int kListCap = 256;    // entries, two tiles of a row's half; a chunk appends up to 32
 constexpr int kListSlack = 16;   // a cut leaves at most K + kListSlack
 constexpr int kSlots = 64;       // per row (at least kMaxTop)
@@ -1180,7 +1186,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           n_blk = item % a.n_nblk;
           m_blk = (item / a.n_nblk) % a.n_mblk;
           part = (item / a.n_nblk) / a.n_mblk;   // DH: this item's K part
-          row0 = (kDwLike<MODE> ? a.out_row0 : (MODE == MODE_DH ? part * a.part_rows : 0)) + m_blk * BMP + static_cast<int>(rank) * BM;
+          row0 = (kDwLike<MODE> ? a.out_row0 : (MODE == MODE_DH ? part * a.part_rows : 0)) + m_blk * BMP +
+                 static_cast<int>(rank) * BM;
           col0 = n_blk * BN + half * 128;
         }
         const int orow = row0 + q * 32;
@@ -1274,6 +1281,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int nval = nv64 >= 64 ? 64 : (nv64 <= 0 ? 0 : static_cast<int>(nv64));
             const int64_t jy64 = y - vc0;
             const int jy = (row_ok && jy64 >= 0 && jy64 < 64) ? static_cast<int>(jy64) : -1;
+            if (vc0 + 64 <= a.pd.V_real) {
+              // Whole chunks: two columns an instruction (as score_grad), rows without
+              // a gradient masked in the packed result, the target's column put in afterwards.
+              const bool any_hit = __any_sync(0xffffffffu, jy >= 0);
+              uint32_t at_y = 0;
+              if (any_hit) {
+                const float zy = jy < 32 ? select32(x0, jy) : select32(x1, jy - 32);
+                at_y = pack_bf16x2(score_grad(sr, zy) + sr.hit, 0.0f) & 0xFFFFu;
+              }
+              const uint64_t s2 = pack_f32x2(sr.s, sr.s), l2 = pack_f32x2(-sr.lse, -sr.lse);
+              const uint64_t e2 = pack_f32x2(sr.ent, sr.ent), c02 = pack_f32x2(sr.c0, sr.c0);
+              const uint64_t c12 = pack_f32x2(sr.c1, sr.c1), k2 = pack_f32x2(kLog2e, kLog2e);
+              const uint32_t keep = row_ok ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+              for (int j = 0; j < 64; j += 2) {
+                const uint32_t xa = j < 32 ? x0[j] : x1[j - 32];
+                const uint32_t xb = j < 32 ? x0[j + 1] : x1[j - 31];
+                const uint64_t lp = fma_f32x2(pack_f32x2(__uint_as_float(xa), __uint_as_float(xb)), s2, l2);
+                float p0, p1, f0, f1, g0, g1;
+                unpack_f32x2(mul_f32x2(lp, k2), p0, p1);
+                unpack_f32x2(add_f32x2(lp, e2), f0, f1);
+                const uint64_t f = fma_f32x2(pack_f32x2(fmaxf(f0, -200.0f), fmaxf(f1, -200.0f)), c12, c02);
+                unpack_f32x2(mul_f32x2(pack_f32x2(ex2_approx(p0), ex2_approx(p1)), f), g0, g1);
+                w[j / 2] = pack_bf16x2(g0, g1) & keep;
+              }
+              if (any_hit) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (2 * i == (jy & ~1)) w[i] = (jy & 1) ? (w[i] & 0xFFFFu) | (at_y << 16) : (w[i] & 0xFFFF0000u) | at_y;
+              }
+              store_box(w, col0 + bb * 64, orow);
+              continue;
+            }
 #pragma unroll
             for (int j = 0; j < 64; j += 2) {
               const uint32_t xa = j < 32 ? x0[j] : x1[j - 32];
