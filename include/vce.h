@@ -378,7 +378,8 @@ vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, c
  * into with VCE_FLAG_ACCUMULATE_DH; dW added into when tied_weights is 1, else
  * overwritten with rows [V_real, Vp) zero). dW_dtype is VCE_F32, or VCE_BF16
  * (bf16 problems, tied_weights 0): the fp32 sum over the tokens rounded once.
- * As in vce_loss_bwd, bf16 problems form G in bf16 for the two products.
+ * As in vce_loss_bwd, bf16 problems form G in bf16 for the two products. A class
+ * whose logit is -inf has G = 0.
  * Workspace: vce_workspace_size(p, VCE_OP_LOGPROB_BWD) bytes recommended, any
  * size from vce_workspace_size_min up accepted.
  */
@@ -395,7 +396,9 @@ vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, c
  *   rstd = 1 / sqrt(mean_i (x_i - mean)^2 + eps),   eps >= 0
  *   y = (x - mean) * rstd * weight + bias, rounded once
  * mean[T] (0 for RMS) and rstd[T] are kept for the backward; either may be
- * NULL. y must not overlap x. Uses p->T, H and dtype. No workspace.
+ * NULL. y must not overlap x. Uses p->T, H and dtype. No workspace. dev_status
+ * (may be NULL) gets VCE_ERR_TIMEOUT if a row's copy did not arrive within the
+ * wait limit; there are no data errors.
  */
 typedef enum vce_norm_kind { VCE_NORM_LAYER = 0, VCE_NORM_RMS = 1 } vce_norm_kind;
 vce_status vce_norm_fwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* bias,
@@ -412,7 +415,7 @@ vce_status vce_norm_fwd(const vce_problem* p, int32_t kind, const void* x, const
  * into dweight and dbias, 0 overwrites them. mean may be NULL for VCE_NORM_RMS.
  * The sums over tokens are taken in an order fixed by the sizes and the device,
  * so results are bit-identical run to run. dx must not overlap x or dy.
- * Workspace: vce_workspace_size(p, VCE_OP_NORM_BWD) bytes.
+ * dev_status as in vce_norm_fwd. Workspace: vce_workspace_size(p, VCE_OP_NORM_BWD) bytes.
  */
 vce_status vce_norm_bwd(const vce_problem* p, int32_t kind, const void* x, const void* weight, const void* dy,
                         const float* mean, const float* rstd, void* dx, float* dweight, float* dbias,

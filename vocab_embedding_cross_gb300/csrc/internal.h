@@ -270,6 +270,16 @@ cudaError_t launch_score_lists(const ScoreLists& sl, int64_t T, int V, int n_uni
                                const int64_t* targets, int64_t ignore_index, float* logp, float* entropy, float* lse,
                                int64_t* top_ids, float* top_logp, int32_t* status, cudaStream_t st);
 // The same from h and W for at most kDecodeTokens tokens (bf16; score_decode.cu).
+// Above, the classes are the MMA's N side and the tokens are padded to 256. Both
+// ways, in us, decode kernel against the wide one (back to back in a graph):
+//   T    H     V       K    decode   wide
+//   65   2048  151936  20    109.0   113.2
+//   128  2048  151936  20    122.3   114.4
+//   128  2048  151936  0     101.5   104.8
+//   128  4096  128000  20    193.0   197.9
+//   128  1024  50000   5      32.1    46.2
+//   100  256   50000   20     20.9    42.1
+// and past 128 tokens the decode kernel would read W twice.
 constexpr int64_t kDecodeTokens = 128;
 size_t score_decode_ws_bytes(const vce_problem& p, int K);
 cudaError_t launch_score_decode(const vce_problem& p, const void* h, const void* W, const int64_t* targets,

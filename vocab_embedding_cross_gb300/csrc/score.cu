@@ -65,7 +65,9 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // One block per token: joins the tensor-core scores' unit statistics and takes
-// the alternatives from the row's list, which holds every logit that can be one.
+// the alternatives from the row's list, which holds every logit that can be one
+// (a few hundred entries of 150000, so 128 threads; T blocks of them take 3 us a
+// thousand tokens beside the 330 us of their product at H = 2048, V = 151936).
 __global__ void __launch_bounds__(kListThreads)
     score_lists_kernel(ScoreLists sl, int V, int n_units, const float* __restrict__ ztgt,
                        const int64_t* __restrict__ targets, int64_t ignore_index, float* __restrict__ logp,

@@ -19,6 +19,18 @@
 // token j's sums in lane j, where its running statistics are kept. The merge
 // kernel joins the CTAs' statistics and takes the alternatives from the
 // 16-class groups whose maximum can reach the K-th largest one.
+//
+// What bounds it: reading W (a kernel that only loads W this way reaches 6.6 to
+// 6.9 TB/s) and, on smaller heads, the start of a launch, the ring's first fill
+// and the merge, 8 to 12 us in all. Both kernels, back to back:
+//   T    H     V       K    us      2 V H bytes at
+//   1    2048  151936  20   103     6.0 TB/s (0.88 of the measured copy rate)
+//   1    2048  151936  0    98.6    6.3 TB/s
+//   48   1024  50257   5    28.5    3.6 TB/s
+//   128  2048  151936  0    101.5   6.1 TB/s
+// The logits' stores (K > 0) cost 25 us at T = 128. With tiles of 16 KB, a ring
+// whose slots held a share of W and of the tokens each, and the feeding loops in
+// one lane, the first of these took 148 us and the third 65 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -319,7 +331,8 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
         for (int b = 0; b < kB; ++b) {
           const int t0 = tok0 + b * kBatch;
           uint32_t x[kBatch];
-          tmem_ld_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>((acc * 2 + sub) * N + t0), x);
+          tmem_ld_x16(tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>((acc * 2 + sub) * N + t0),
+                      x);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < kBatch; ++j) asm volatile("" : "+r"(x[j]));
@@ -341,12 +354,14 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
           const float hm = butterfly16<true>(mx, lane);
           const float gm = fmaxf(hm, other_half(hm));
           if (a.gmax && t0 + (lane & 15) < a.T && r0 + (lane & 16) < row_hi)
-            a.gmax[static_cast<int64_t>(t0 + (lane & 15)) * a.ldg + ((r0 + lane) >> 4)] = hm == hm ? ordered_bits(hm) : 0u;
+            a.gmax[static_cast<int64_t>(t0 + (lane & 15)) * a.ldg + ((r0 + lane) >> 4)] =
+                hm == hm ? ordered_bits(hm) : 0u;
           const int64_t off = y[b] - r0;                  // the target, if it is one of the warp's classes
-          if (__any_sync(0xffffffffu, off >= 0 && off < 32)) {
+          const int mine = off >= 0 && off < 32 ? static_cast<int>(off) : -1;
+          if (__any_sync(0xffffffffu, mine >= 0)) {
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
-              const int at = static_cast<int>(__shfl_sync(0xffffffffu, off >= 0 && off < 32 ? static_cast<int>(off) : -1, j));
+              const int at = __shfl_sync(0xffffffffu, mine, j);
               if (at == lane && row_ok) a.ztgt[t0 + j] = __uint_as_float(x[j]);
             }
           }
@@ -371,7 +386,8 @@ __global__ void __launch_bounds__(Dec<N>::threads, 1)
     for (int b = 0; b < kB; ++b) {
       const int t = tok0 + b * kBatch + lane;
       if (lane < kBatch && t < a.T)
-        a.part[(static_cast<int64_t>(t) * n_cta + cta) * D::parts + sub0 * 4 + q] = make_float4(m_run[b], s_run[b], u_run[b], 0.0f);
+        a.part[(static_cast<int64_t>(t) * n_cta + cta) * D::parts + sub0 * 4 + q] =
+            make_float4(m_run[b], s_run[b], u_run[b], 0.0f);
     }
   }
   __syncwarp();
@@ -392,7 +408,8 @@ constexpr int kMergeKeep = 3;      // quadruples of group maxima that each threa
 // disjoint lists' best ones bounds the K-th largest key of the row from below; only
 // groups that reach (g, first class) >= the bound are read, one half-warp each.
 // Equal logits do not widen the choice: an all-equal row reads about the first
-// K groups.
+// K groups. Bound by the latency of its steps (read statistics and maxima, bound,
+// read groups, rank): 3 to 5 us behind the decode kernel, which lets it set up early.
 __global__ void __launch_bounds__(kMergeThreads)
     score_merge_kernel(int V, int groups, int ldg, int n_part, const float4* __restrict__ part,
                        const uint32_t* __restrict__ gmax, const float* __restrict__ Z, int64_t ldz,
@@ -447,8 +464,8 @@ __global__ void __launch_bounds__(kMergeThreads)
 #pragma unroll
   for (int c = 0; c < kMergeKeep; ++c) raise(keep[c], tid + c * kMergeThreads);
   for (int quad = tid + kMergeKeep * kMergeThreads; quad < quads; quad += kMergeThreads) raise(words(quad), quad);
-  const uint64_t kmax =
-      most ? (static_cast<uint64_t>(most) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(min(64 * most_at + 64, V) - 1)) : 0;
+  const uint32_t most_last = static_cast<uint32_t>(min(64 * most_at + 64, V) - 1);
+  const uint64_t kmax = most ? (static_cast<uint64_t>(most) << 32) | (0xFFFFFFFFu - most_last) : 0;
   if (K) top_raise(top, kmax);
   a = block_join(a, sh);
   const float l = score_lse(a);
@@ -464,7 +481,8 @@ __global__ void __launch_bounds__(kMergeThreads)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       // the key that the group's first class would have with the group's maximum
-      const uint64_t k = (static_cast<uint64_t>(w[j]) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(64 * quad + 16 * j));
+      const uint32_t first = static_cast<uint32_t>(64 * quad + 16 * j);
+      const uint64_t k = (static_cast<uint64_t>(w[j]) << 32) | (0xFFFFFFFFu - first);
       if (w[j] != 0 && k >= bound) {
         const int at = atomicAdd(&s_pick, 1);
         if (at < kMergePick) pick[at] = 4 * quad + j;
@@ -566,9 +584,9 @@ cudaError_t launch_score_decode(const vce_problem& p, const void* h, const void*
                               : launch_n<128>(p, h, W, L, a, st);
   if (e != cudaSuccess) return e;
   e = launch_dependent(score_merge_kernel, dim3(static_cast<unsigned>(p.T)), dim3(kMergeThreads), 0, st, a.V, L.groups,
-                       L.ldg, L.parts * L.n_cta, static_cast<const float4*>(a.part), static_cast<const uint32_t*>(a.gmax),
-                       static_cast<const float*>(a.Z), a.ldz, static_cast<const float*>(a.ztgt), targets,
-                       p.ignore_index, scale, K, logp, entropy, lse, top_ids, top_logp, status);
+                       L.ldg, L.parts * L.n_cta, static_cast<const float4*>(a.part),
+                       static_cast<const uint32_t*>(a.gmax), static_cast<const float*>(a.Z), a.ldz,
+                       static_cast<const float*>(a.ztgt), targets, p.ignore_index, scale, K, logp, entropy, lse, top_ids, top_logp, status);
   note_launch(VCE_K_SCORE_MERGE, st);
   return e;
 }

@@ -9,7 +9,10 @@
 // next slice is fetched into registers while the current one is multiplied out of
 // one of two shared-memory buffers. Small heads are bound by latency, so the
 // parts of DH matter more than the inner loop: one 64 x 64 tile over K = 1000 as
-// one block took 61 us.
+// one block took 61 us. T = 64, H = 64, V = 1000: scores 13 us and gradient 20 us a
+// call, launches and host included; T = 300, H = 512, V = 8000: gradient 267 us,
+// 28 TFLOP/s of fp32 FMA, bound by shared-memory reads (two 16-byte loads for 16
+// FMA). fp32 heads are kept for checks; the tensor cores have no fp32 form.
 //
 // The parts are joined, in a fixed order, by join_kernel, which also serves the
 // tensor-core path's dH.
@@ -144,7 +147,8 @@ __global__ void __launch_bounds__(256) f32_product_kernel(const F32Args a) {
         const int n = n0 + 4 * tx + j;
         const float lp = fmaf(acc[i][j], a.sg.scale, -lse);
         const float p = expf(lp);
-        const float g = a.sg.scale * (gl * ((a.v0 + n == y ? 1.0f : 0.0f) - p) - ge * p * fmaxf(lp + ent, -200.0f));   // p is 0 below
+        const float f = fmaxf(lp + ent, -200.0f);   // p is 0 below: a logit of -inf gives 0
+        const float g = a.sg.scale * (gl * ((a.v0 + n == y ? 1.0f : 0.0f) - p) - ge * p * f);
         acc[i][j] = valid ? g : 0.0f;
       }
     }
@@ -297,8 +301,8 @@ cudaError_t launch_join(const float* P, int64_t part_elems, int parts, const flo
   const int64_t n4 = n / 4, want = ceil_div(n4, 32), cap = static_cast<int64_t>(current_device_info().num_sms) * 8;
   const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
   auto go = [&](auto kern, auto* to) {
-    return launch_dependent(kern, grid, dim3(32 * kJoinLanes), 0, st, reinterpret_cast<const float4*>(P), part_elems / 4, parts,
-                            reinterpret_cast<const float4*>(before), add ? 1 : 0, to, n4);
+    return launch_dependent(kern, grid, dim3(32 * kJoinLanes), 0, st, reinterpret_cast<const float4*>(P),
+                            part_elems / 4, parts, reinterpret_cast<const float4*>(before), add ? 1 : 0, to, n4);
   };
   const cudaError_t e = out_bf16 ? go(join_kernel<uint2>, static_cast<uint2*>(out))
                                  : go(join_kernel<float4>, static_cast<float4*>(out));
