@@ -279,7 +279,8 @@ def run_bwd(dtype, h, W, y, V, Vp, ref, gl, ge, scale, flags=0, tied=False, dH=N
     return dH, dW
 
 
-def check_bwd(dtype, got, h, W, y, V, ref, gl, ge, scale, dh_bf16=False, dw_bf16=False, base=(0.0, 0.0)):
+def check_bwd(dtype, got, h, W, y, V, ref, gl, ge, scale, dh_bf16=False, dw_bf16=False, base=(0.0, 0.0),
+              g_round=2.0 ** -8):
     hf, Wf = S.as_f64(h), S.as_f64(W)
     T = hf.shape[0]
     ok = np.ones(T, bool) if y is None else S.valid_targets(y, V)
@@ -297,7 +298,7 @@ def check_bwd(dtype, got, h, W, y, V, ref, gl, ge, scale, dh_bf16=False, dw_bf16
         Gabs[np.arange(T), np.where(ok, y, 0)] += glv
     Gabs *= scale
     A = np.abs(scale * ref["z"][ok]).max() if ok.any() else 0.0
-    dG = ((8 * A + 80) + 2 * A) * U24 * Gabs + (2.0 ** -8 * np.abs(G) if dtype == "bf16" else 0)
+    dG = ((8 * A + 80) + 2 * A) * U24 * Gabs + (g_round * np.abs(G) if dtype == "bf16" else 0)
     for name, x, g, b, n, wide, pre in (("dH", got[0], G @ Wf[:V], dG @ np.abs(Wf[:V]) , V, dh_bf16, base[0]),
                                         ("dW", got[1][:V], G.T @ hf, dG.T @ np.abs(hf), T, dw_bf16, base[1])):
         mag = np.abs(G) @ np.abs(Wf[:V]) if name == "dH" else np.abs(G).T @ np.abs(hf)
@@ -326,6 +327,25 @@ def test_gradient(dtype, T, H, V, S_, scale, terms):
     check_bwd(dtype, got, h, W, y, V, ref, gl, ge, scale)
     assert not got[1][V:].any().item()                    # padding rows of an untied dW are zero
     assert not got[0][torch.from_numpy(y < 0).cuda()].any().item()
+
+
+@pytest.mark.parametrize("T", [1, 9, 31, 32, 33, 64, 100, 128])
+@pytest.mark.parametrize("how", ["stored", "added", "chunks", "no targets"])
+def test_gradient_of_few_tokens_keeps_what_rounding_left(T, how):
+    """Up to 128 tokens G is the sum of two bf16 values: half a step of half a step, 2^-16, is lost."""
+    H, V = 200, 4001
+    h, W, y, Vp = grid_case(T, H, V, "bf16", seed=17)
+    rng = np.random.default_rng([18, T])
+    gl, ge = (rng.standard_normal(T).astype(np.float32).astype(np.float64) * s for s in (1.0, 0.25))
+    if how == "no targets":
+        y = gl = None
+    ref = S.token_scores(h, W, y, V, 1.25)
+    added = how == "added"
+    dH, dW = torch.full((T, H), 2.0, device="cuda"), torch.full((Vp, H), -1.5, device="cuda")
+    got = run_bwd("bf16", h, W, y, V, Vp, ref, gl, ge, 1.25, flags=vce.VCE_FLAG_ACCUMULATE_DH if added else 0,
+                  tied=added, dH=dH if added else None, dW=dW if added else None, minimal=how == "chunks")
+    check_bwd("bf16", got, h, W, y, V, ref, gl, ge, 1.25, base=(2.0, -1.5) if added else (0.0, 0.0),
+              g_round=2.0 ** -16)
 
 
 @pytest.mark.parametrize("dtype,T", [("bf16", 7), ("bf16", 300), ("f32", 65)])

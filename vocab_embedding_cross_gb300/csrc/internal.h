@@ -93,7 +93,16 @@ struct ScoreBwd {
   void* hm;
   float* P;
   bool dW_bf16;
+  int lo_rows;   // 0, or G and hm have a second half from this row on (score_lo_rows)
 };
+// Up to 128 tokens leave half of a 256-row MMA tile to padding. There the rows from
+// lo_rows on hold what the bf16 rounding of G left, rounded to bf16 again, and the
+// same tokens' h a second time, so that both products take G to 2^-16 instead of
+// 2^-8 (a gradient of a few tokens is mostly its targets' elements, whose rounding
+// errors nothing averages).
+inline int64_t score_lo_rows(const vce_problem& p) {
+  return p.dtype == VCE_BF16 && p.T <= 128 ? (p.T + 31) / 32 * 32 : 0;
+}
 
 // Statistics and lists of alternatives of the tensor-core scores.
 struct ScoreLists {
@@ -295,9 +304,10 @@ cudaError_t launch_f32_logits(const ProbDev& pd, const float* h, const float* W,
 cudaError_t launch_f32_score_bwd(const ProbDev& pd, const float* h, const float* W, const int64_t* targets,
                                  const ScoreGrad& sg, int v0, int vc, float* G, int64_t ldg, float* P, int parts,
                                  float* dH, bool dH_add, float* dW, bool dW_add, int32_t* status, cudaStream_t st);
-// out[0..n) (+)= before + the parts in order (fp32 or bf16; n a multiple of 4; before may be null).
-cudaError_t launch_join(const float* P, int64_t part_elems, int parts, const float* before, bool add, void* out,
-                        bool out_bf16, int64_t n, cudaStream_t st);
+// out[0..n) (+)= before + the parts in order (fp32 or bf16; n a multiple of 4; before
+// may be null), each part with its second summand lo_elems on, if that is not 0.
+cudaError_t launch_join(const float* P, int64_t part_elems, int64_t lo_elems, int parts, const float* before, bool add,
+                        void* out, bool out_bf16, int64_t n, cudaStream_t st);
 
 // Layer and RMS normalisation (norm.cu).
 size_t norm_ws_bytes(const vce_problem& p);

@@ -128,6 +128,7 @@ struct TcArgs {
   ScoreGrad sg;         // SGRAD: what the forward scores left and their upstream gradients
   const uint4* h16;     // SGRAD: h, and where it is copied without the rows of tokens
   uint4* hm16;          // that have no gradient (or null)
+  int lo_rows;          // SGRAD: 0, or the odd CTA writes what rounding left of the even one's rows
   ScoreLists sl;        // SCORE: statistics, scale and the lists of alternatives
 };
 
@@ -190,7 +191,7 @@ __device__ __forceinline__ TileCoord tile_coord(const TcArgs& a, int item, int t
     c.bn = static_cast<int32_t>(us.vb + static_cast<int64_t>(tt) * BN) + rank * BNH;
   } else if constexpr (kGradLike<MODE>) {
     const MC mc = item_mc(item, a.gm, a.n_mblk, a.n_cols);
-    c.am = mc.m * BMP + rank * BM;
+    c.am = mc.m * BMP + (MODE == MODE_SGRAD && a.lo_rows ? 0 : rank * BM);
     c.bn = a.v0 + mc.c * BN + rank * BNH;
   } else {
     const int n_blk = item % a.n_nblk, m_blk = (item / a.n_nblk) % a.n_mblk;
@@ -752,7 +753,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // for G^T h, which must not multiply a zero of G by what such a row holds.
       if (a.hm16) {
         const int row16 = a.pd.H / 8;
-        const int64_t n16 = static_cast<int64_t>(a.pd.T) * row16;
+        const int64_t n16 = static_cast<int64_t>(a.lo_rows ? 2 * a.lo_rows : a.pd.T) * row16;
         const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kEpiWarps);
         for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * (32 * kEpiWarps) + threadIdx.x - 64; i0 < n16;
              i0 += 4 * step) {
@@ -761,10 +762,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int64_t i = i0 + j * step;
-            const int64_t y = i < n16 ? __ldg(a.targets + i / row16) : a.pd.ignore_index;
-            take[j] = y >= 0 && y < a.pd.V_real;
+            const int row = static_cast<int>(i / row16);
+            const int second = a.lo_rows && row >= a.lo_rows ? a.lo_rows : 0;   // the rows repeat from lo_rows on
+            const bool real = i < n16 && row - second < a.pd.T;
+            const int64_t y = !real ? a.pd.ignore_index : a.targets ? __ldg(a.targets + (row - second)) : 0;
+            take[j] = real && y >= 0 && y < a.pd.V_real;
             if (!take[j] && y != a.pd.ignore_index) record_status(a.status, VCE_ERR_BAD_INDEX);
-            if (i < n16) v[j] = __ldg(a.h16 + i);
+            if (real) v[j] = __ldg(a.h16 + (i - static_cast<int64_t>(second) * row16));
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -1256,7 +1260,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             store_box(w, col0 + bb * 64, orow);
           }
         } else if constexpr (MODE == MODE_SGRAD) {
-          const int t = m_blk * BMP + static_cast<int>(rank) * BM + r;
+          const bool lo = a.lo_rows && rank == 1;
+          const int t = a.lo_rows ? r : m_blk * BMP + static_cast<int>(rank) * BM + r;
+          const int grow = a.lo_rows ? (lo ? a.lo_rows : 0) + q * 32 : orow;   // G's row of lane 0
+          const bool stores = !a.lo_rows || q * 32 < a.lo_rows;
           int64_t y = -1;
           bool row_ok = false;
           ScoreGradRow sr{};
@@ -1288,7 +1295,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               uint32_t at_y = 0;
               if (any_hit) {
                 const float zy = jy < 32 ? select32(x0, jy) : select32(x1, jy - 32);
-                at_y = pack_bf16x2(score_grad(sr, zy) + sr.hit, 0.0f) & 0xFFFFu;
+                const float gy = score_grad(sr, zy) + sr.hit;
+                at_y = pack_bf16x2(gy, 0.0f);
+                if (lo) at_y = pack_bf16x2(gy - __uint_as_float(at_y << 16), 0.0f);
+                at_y &= 0xFFFFu;
               }
               const uint64_t s2 = pack_f32x2(sr.s, sr.s), l2 = pack_f32x2(-sr.lse, -sr.lse);
               const uint64_t e2 = pack_f32x2(sr.ent, sr.ent), c02 = pack_f32x2(sr.c0, sr.c0);
@@ -1304,14 +1314,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 unpack_f32x2(add_f32x2(lp, e2), f0, f1);
                 const uint64_t f = fma_f32x2(pack_f32x2(fmaxf(f0, -200.0f), fmaxf(f1, -200.0f)), c12, c02);
                 unpack_f32x2(mul_f32x2(pack_f32x2(ex2_approx(p0), ex2_approx(p1)), f), g0, g1);
-                w[j / 2] = pack_bf16x2(g0, g1) & keep;
+                w[j / 2] = pack_bf16x2(g0, g1);
+                if (lo)
+                  w[j / 2] = pack_bf16x2(g0 - __uint_as_float(w[j / 2] << 16),
+                                         g1 - __uint_as_float(w[j / 2] & 0xFFFF0000u));
+                w[j / 2] &= keep;
               }
               if (any_hit) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (2 * i == (jy & ~1)) w[i] = (jy & 1) ? (w[i] & 0xFFFFu) | (at_y << 16) : (w[i] & 0xFFFF0000u) | at_y;
               }
-              store_box(w, col0 + bb * 64, orow);
+              if (stores) store_box(w, col0 + bb * 64, grow);
               continue;
             }
 #pragma unroll
@@ -1324,8 +1338,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (j == jy) g0 += sr.hit;
               if (j + 1 == jy) g1 += sr.hit;
               w[j / 2] = pack_bf16x2(g0, g1);
+              if (lo)
+                w[j / 2] = pack_bf16x2(g0 - __uint_as_float(w[j / 2] << 16),
+                                       g1 - __uint_as_float(w[j / 2] & 0xFFFF0000u));
             }
-            store_box(w, col0 + bb * 64, orow);
+            if (stores) store_box(w, col0 + bb * 64, grow);
           }
         } else if constexpr (MODE == MODE_DWB) {
           // The whole sum over the tokens is in this one accumulator: rounded
@@ -1650,6 +1667,7 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
   float* const P = sb ? sb->P : nullptr;
   const int64_t part_rows = ceil_div(p.T, BMP) * BMP;
   const int parts = dh_flags || P ? dh_parts : 1;
+  const uint64_t g_rows = sb && sb->lo_rows ? 2 * sb->lo_rows : p.T;   // rows of G and of hm
   const int n_flags = static_cast<int>(ceil_div(p.T, BMP) * ceil_div(p.H, BN)) * 2 * kEpiWarps;
   const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto F32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
@@ -1659,7 +1677,7 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     CUtensorMap mh, mw, mg;
     if (!make_tmap_2d(&mh, h, BF, 2, p.H, p.T, p.H, 64, BM, true) ||
         !make_tmap_2d(&mw, W, BF, 2, p.H, p.V_real, p.H, 64, BNH, true) ||
-        !make_tmap_2d(&mg, G, BF, 2, vc_act, p.T, g_ld, 64, 32, true))
+        !make_tmap_2d(&mg, G, BF, 2, vc_act, g_rows, g_ld, 64, 32, true))
       return cudaErrorInvalidValue;
     TcArgs a = base_args(p, targets, status);
     a.n_mblk = static_cast<int>(ceil_div(p.T, BMP));
@@ -1676,6 +1694,7 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     a.n_dh_flags = parts > 1 && dh_flags ? n_flags : 0;
     if (sb) {
       a.sg = sb->sg;
+      a.lo_rows = sb->lo_rows;
       a.h16 = static_cast<const uint4*>(h);
       a.hm16 = v0 == 0 ? static_cast<uint4*>(sb->hm) : nullptr;   // once, with the first column chunk
       e = launch_mode<MODE_SGRAD>(mh, mw, mg, a, st);
@@ -1689,7 +1708,7 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
   // before it (counters in dh_flags), so the order of the additions is fixed.
   {
     CUtensorMap mg, mw, mo;
-    if (!make_tmap_2d(&mg, G, BF, 2, vc_act, p.T, g_ld, 64, BM, true) ||
+    if (!make_tmap_2d(&mg, G, BF, 2, vc_act, g_rows, g_ld, 64, BM, true) ||
         !make_tmap_2d(&mw, W, BF, 2, p.H, p.V_real, p.H, 64, 64, true) ||
         !make_tmap_2d(&mo, P ? P : dH, F32, 4, p.H, P ? part_rows * parts : p.T, p.H, 32, 32, true))
       return cudaErrorInvalidValue;
@@ -1710,8 +1729,8 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
   // DW: dW[v0:v0+vc_act, :] (+)= G[:, 0:vc_act]^T h
   {
     CUtensorMap mg, mh, mo;
-    if (!make_tmap_2d(&mg, G, BF, 2, vc_act, p.T, g_ld, 64, 64, true) ||
-        !make_tmap_2d(&mh, sb && sb->hm ? sb->hm : h, BF, 2, p.H, p.T, p.H, 64, 64, true) ||
+    if (!make_tmap_2d(&mg, G, BF, 2, vc_act, g_rows, g_ld, 64, 64, true) ||
+        !make_tmap_2d(&mh, sb && sb->hm ? sb->hm : h, BF, 2, p.H, g_rows, p.H, 64, 64, true) ||
         !make_tmap_2d(&mo, dW, dW_bf16 ? BF : F32, dW_bf16 ? 2 : 4, p.H, static_cast<uint64_t>(v0) + vc_act, p.H,
                       dW_bf16 ? 64 : 32, 32, true))
       return cudaErrorInvalidValue;
@@ -1719,7 +1738,7 @@ cudaError_t launch_tc_bwd_chunk(const vce_problem& p, const void* h, const void*
     a.n_mblk = static_cast<int>(ceil_div(vc_act, BMP));
     a.n_nblk = static_cast<int>(ceil_div(p.H, BN));
     a.n_items = a.n_mblk * a.n_nblk;
-    a.num_kb = static_cast<int>(ceil_div(p.T, BK));
+    a.num_kb = static_cast<int>(ceil_div(static_cast<int64_t>(g_rows), BK));
     a.out_row0 = v0;
     a.accumulate = dW_accumulate ? 1 : 0;
     e = dW_bf16 ? launch_mode<MODE_DWB>(mg, mh, mo, a, st) : launch_mode<MODE_DW>(mg, mh, mo, a, st);

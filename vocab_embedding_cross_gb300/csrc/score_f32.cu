@@ -162,12 +162,13 @@ __global__ void __launch_bounds__(256) f32_product_kernel(const F32Args a) {
 // out[t, i] (+)= before + the sum of the parts, rounded once. A block takes 32
 // quadruples of columns with eight threads each, which add every eighth part; their
 // sums are added in order (one thread a quadruple took 13 us to add 76 parts).
-// parts are P[part][rows][H], rows >= T.
+// parts are P[part][rows][H], rows >= T; with lo4, each has a second summand that
+// many quadruples further on (score_lo_rows).
 constexpr int kJoinLanes = 8;
 template <typename O>
 __global__ void __launch_bounds__(32 * kJoinLanes)
-    join_kernel(const float4* __restrict__ P, int64_t part4, int parts, const float4* __restrict__ before, int add,
-                O* __restrict__ out, int64_t n4) {
+    join_kernel(const float4* __restrict__ P, int64_t part4, int64_t lo4, int parts, const float4* __restrict__ before,
+                int add, O* __restrict__ out, int64_t n4) {
   __shared__ float4 sh[kJoinLanes][32];
   grid_dep_launch();
   grid_dep_wait();
@@ -178,7 +179,11 @@ __global__ void __launch_bounds__(32 * kJoinLanes)
     if (i < n4) {
 #pragma unroll 4
       for (int p = y; p < parts; p += kJoinLanes) {
-        const float4 v = P[p * part4 + i];
+        float4 v = P[p * part4 + i];
+        if (lo4) {
+          const float4 l = P[p * part4 + lo4 + i];
+          v = make_float4(v.x + l.x, v.y + l.y, v.z + l.z, v.w + l.w);
+        }
         a.x += v.x;
         a.y += v.y;
         a.z += v.z;
@@ -296,13 +301,13 @@ cudaError_t launch_f32_score_bwd(const ProbDev& pd, const float* h, const float*
   return launch_form<DW>(a, 1, VCE_K_SGEMM, st);
 }
 
-cudaError_t launch_join(const float* P, int64_t part_elems, int parts, const float* before, bool add, void* out,
-                        bool out_bf16, int64_t n, cudaStream_t st) {
+cudaError_t launch_join(const float* P, int64_t part_elems, int64_t lo_elems, int parts, const float* before, bool add,
+                        void* out, bool out_bf16, int64_t n, cudaStream_t st) {
   const int64_t n4 = n / 4, want = ceil_div(n4, 32), cap = static_cast<int64_t>(current_device_info().num_sms) * 8;
   const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
   auto go = [&](auto kern, auto* to) {
     return launch_dependent(kern, grid, dim3(32 * kJoinLanes), 0, st, reinterpret_cast<const float4*>(P),
-                            part_elems / 4, parts, reinterpret_cast<const float4*>(before), add ? 1 : 0, to, n4);
+                            part_elems / 4, lo_elems / 4, parts, reinterpret_cast<const float4*>(before), add ? 1 : 0, to, n4);
   };
   const cudaError_t e = out_bf16 ? go(join_kernel<uint2>, static_cast<uint2*>(out))
                                  : go(join_kernel<float4>, static_cast<float4*>(out));

@@ -257,10 +257,16 @@ size_t score_ws_bytes(const vce_problem& p, int K) {
 // as the loss backward's) stand the fp32 sum of a bf16 dH, the bf16 path's copy of
 // h without the rows of ignored tokens, and the parts of a dH with few tiles.
 struct ScoreBwdLayout {
-  size_t acc, hm, P, front;
+  size_t acc, hm, P, front;   // P == front: none
   int parts;
-  int64_t part_elems;
+  int64_t part_elems, lo_rows;
 };
+// What G is sized by: with the rows from lo_rows on, where there are any.
+vce_problem score_g_problem(const vce_problem& p) {
+  vce_problem q = p;
+  if (score_lo_rows(p)) q.T = 2 * score_lo_rows(p);
+  return q;
+}
 ScoreBwdLayout score_bwd_layout(const vce_problem& p) {
   ScoreBwdLayout L{};
   const size_t T = static_cast<size_t>(p.T), H = static_cast<size_t>(p.H);
@@ -268,10 +274,11 @@ ScoreBwdLayout score_bwd_layout(const vce_problem& p) {
   L.parts = p.T == 0 ? 1 : bf16 ? tc_dh_stored_parts(p) : f32_dh_parts(p.T, p.H, p.V_real);
   const size_t rows = bf16 ? (T + 255) / 256 * 256 : T;
   L.part_elems = static_cast<int64_t>(rows * H);
+  L.lo_rows = score_lo_rows(p);
   L.acc = 0;
   L.hm = dh_acc_bytes(p);
-  L.P = L.hm + (bf16 ? align_up(T * H * 2, kWsAlign) : 0);
-  L.front = L.P + (L.parts > 1 ? align_up(static_cast<size_t>(L.parts) * rows * H * 4, kWsAlign) : 0);
+  L.P = L.hm + (bf16 ? align_up(static_cast<size_t>(score_g_problem(p).T) * H * 2, kWsAlign) : 0);
+  L.front = L.P + (L.parts > 1 || L.lo_rows ? align_up(static_cast<size_t>(L.parts) * rows * H * 4, kWsAlign) : 0);
   return L;
 }
 
@@ -394,8 +401,10 @@ size_t vce_workspace_size(const vce_problem* p, int32_t op) {
       return dh_acc_bytes(*p) + bwd_bytes_for(*p, bwd_recommended_cols(*p)) + dh_flag_bytes(*p);
     case VCE_OP_SAMPLED_CANDIDATES: return sampled_ws_bytes(*p);
     case VCE_OP_GREEDY_ARGMAX: return argmax_ws_bytes(*p);
-    case VCE_OP_LOGPROB_BWD:
-      return score_bwd_layout(*p).front + bwd_bytes_for(*p, bwd_recommended_cols(*p)) + dh_flag_bytes(*p);
+    case VCE_OP_LOGPROB_BWD: {
+      const vce_problem g = score_g_problem(*p);
+      return score_bwd_layout(*p).front + bwd_bytes_for(g, bwd_recommended_cols(g)) + dh_flag_bytes(*p);
+    }
     case VCE_OP_NORM_BWD: return norm_ws_bytes(*p);
   }
   return SIZE_MAX;
@@ -405,7 +414,7 @@ size_t vce_workspace_size_min(const vce_problem* p, int32_t op) {
   if (check_problem(p) != VCE_OK) return SIZE_MAX;
   if (op == VCE_OP_LOSS_BWD) return dh_acc_bytes(*p) + bwd_bytes_for(*p, p->T == 0 ? 0 : 256);
   if (op == VCE_OP_LOGPROB_BWD)
-    return score_bwd_layout(*p).front + bwd_bytes_for(*p, p->T == 0 ? 0 : 256);
+    return score_bwd_layout(*p).front + bwd_bytes_for(score_g_problem(*p), p->T == 0 ? 0 : 256);
   return vce_workspace_size(p, op);
 }
 
@@ -770,19 +779,21 @@ vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, c
   char* b = front + L.front;
   ws_bytes -= L.front;
   const bool bf16 = p->dtype == VCE_BF16, dH_bf16 = (p->flags & VCE_FLAG_DH_BF16) != 0;
-  const size_t part_bytes = L.parts > 1 ? 0 : dh_flag_bytes(*p);
-  const bool use_flags = part_bytes > 0 && ws_bytes >= bwd_bytes_for(*p, 256) + part_bytes;
-  int64_t vc = bwd_chunk_cols(*p, use_flags ? ws_bytes - part_bytes : ws_bytes);
+  const vce_problem gp = score_g_problem(*p);
+  const size_t part_bytes = L.P < L.front ? 0 : dh_flag_bytes(*p);
+  const bool use_flags = part_bytes > 0 && ws_bytes >= bwd_bytes_for(gp, 256) + part_bytes;
+  int64_t vc = bwd_chunk_cols(gp, use_flags ? ws_bytes - part_bytes : ws_bytes);
   if (vc < 256) return VCE_ERR_WORKSPACE;
   int32_t* status = dev_status;   // may be null: data errors then go unreported
   int32_t* dh_flags = use_flags ? reinterpret_cast<int32_t*>(b + kBwdHeader) : nullptr;
   void* G = b + kBwdHeader + (use_flags ? part_bytes : 0);
   const ProbDev pd = prob_dev(*p);
   const ScoreGrad sg{lse, entropy, g_logp, g_entropy, logit_scale};
-  float* P = L.parts > 1 ? reinterpret_cast<float*>(front + L.P) : nullptr;
+  float* P = L.P < L.front ? reinterpret_cast<float*>(front + L.P) : nullptr;
   // The fp32 dH: the caller's, or the sum of a bf16 one.
   float* dH = dH_bf16 ? reinterpret_cast<float*>(front + L.acc) : static_cast<float*>(dH_out);
-  ScoreBwd sb{sg, targets ? front + L.hm : nullptr, P, dW_dtype == VCE_BF16};
+  ScoreBwd sb{sg, targets || L.lo_rows ? front + L.hm : nullptr, P, dW_dtype == VCE_BF16,
+              static_cast<int>(L.lo_rows)};
   if (!p->tied_weights && p->Vp > p->V_real) {
     if (cudaError_t me = cudaMemsetAsync(static_cast<char*>(dW) + row_bytes * p->V_real, 0,
                                          row_bytes * (p->Vp - p->V_real), st))
@@ -800,7 +811,7 @@ vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, c
       if (P) {   // every part of this chunk's K blocks (64 columns) has at least one
         const int64_t kb = ceil_div(vc_act, 64);
         parts = static_cast<int>(ceil_div(kb, ceil_div(kb, L.parts)));
-        sb.P = parts > 1 ? P : nullptr;
+        sb.P = parts > 1 || L.lo_rows ? P : nullptr;
       } else if (dh_flags) {
         parts = tc_dh_parts(*p, vc_act);
       }
@@ -812,14 +823,16 @@ vce_status vce_logprob_bwd(const vce_problem* p, const void* h, const void* W, c
                                static_cast<int>(c0), vc_act, static_cast<float*>(G), vc, P, parts, dH, add,
                                static_cast<float*>(dW), p->tied_weights != 0, status, st);
     }
-    if (e == cudaSuccess && P && parts > 1) {
+    const bool join = P && (parts > 1 || L.lo_rows);
+    if (e == cudaSuccess && join) {
+      const int64_t lo = L.lo_rows * p->H;
       if (dH_bf16 && last)
-        e = launch_join(P, L.part_elems, parts, c0 > 0 ? dH : nullptr, acc_out, dH_out, true, n, st);
+        e = launch_join(P, L.part_elems, lo, parts, c0 > 0 ? dH : nullptr, acc_out, dH_out, true, n, st);
       else
-        e = launch_join(P, L.part_elems, parts, nullptr, add, dH, false, n, st);
+        e = launch_join(P, L.part_elems, lo, parts, nullptr, add, dH, false, n, st);
     }
     if (e != cudaSuccess) return cuda_status(e);
-    if (dH_bf16 && last && !(P && parts > 1)) return cuda_status(launch_dh_to_bf16(dH, dH_out, n, acc_out, st));
+    if (dH_bf16 && last && !join) return cuda_status(launch_dh_to_bf16(dH, dH_out, n, acc_out, st));
   }
   return VCE_OK;
 }
