@@ -378,8 +378,9 @@ vce_status vce_logprob_fwd(const vce_problem* p, const void* h, const void* W, c
  * into with VCE_FLAG_ACCUMULATE_DH; dW added into when tied_weights is 1, else
  * overwritten with rows [V_real, Vp) zero). dW_dtype is VCE_F32, or VCE_BF16
  * (bf16 problems, tied_weights 0): the fp32 sum over the tokens rounded once.
- * As in vce_loss_bwd, bf16 problems form G in bf16 for the two products. A class
- * whose logit is -inf has G = 0.
+ * As in vce_loss_bwd, bf16 problems form G in bf16 for the two products; up to 128
+ * tokens it is the sum of two bf16 values, kept to 2^-16. A class whose logit is
+ * -inf has G = 0.
  * Workspace: vce_workspace_size(p, VCE_OP_LOGPROB_BWD) bytes recommended, any
  * size from vce_workspace_size_min up accepted.
  */

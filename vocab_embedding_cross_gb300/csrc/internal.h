@@ -99,7 +99,9 @@ struct ScoreBwd {
 // lo_rows on hold what the bf16 rounding of G left, rounded to bf16 again, and the
 // same tokens' h a second time, so that both products take G to 2^-16 instead of
 // 2^-8 (a gradient of a few tokens is mostly its targets' elements, whose rounding
-// errors nothing averages).
+// errors nothing averages). H = 1024, V = 50257, in us with and without: T = 16 86.3
+// and 82.7, T = 64 88.8 and 82.4, T = 128 98.4 and 89.2; from 129 tokens on it would
+// cost a second tile of each product.
 inline int64_t score_lo_rows(const vce_problem& p) {
   return p.dtype == VCE_BF16 && p.T <= 128 ? (p.T + 31) / 32 * 32 : 0;
 }

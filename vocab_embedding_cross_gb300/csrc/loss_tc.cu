@@ -274,6 +274,10 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
 // logp is one rounding of s z - lse before anything else is added, so that it
 // keeps its relative precision in peaked rows, where it is near 0. The factor of p
 // is held above -200, where p is 0 in fp32, so that a logit of -inf gives 0.
+//
+// SGRAD is bound by the tensor cores: at T = 8192, H = 2048, 76032 columns take 1.57 ms,
+// the product alone 1.36 at the measured burst rate; T = 2048, H = 1024, V = 50000: 134 us
+// and 112 (148 us with the epilogue below one column an instruction).
 struct ScoreGradRow {
   float s, lse, ent, c0, c1, hit;
 };
@@ -1346,7 +1350,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         } else if constexpr (MODE == MODE_DWB) {
           // The whole sum over the tokens is in this one accumulator: rounded
-          // to bf16 once, 64 columns to a 128-byte row of the store box.
+          // to bf16 once, 64 columns to a 128-byte row of the store box. T = 2048,
+          // H = 1024, V = 50000: 127 us, where the product needs 112; T = 64: 31 us for
+          // 103 MB, bound by each tile's chain from the accumulator to the store (both
+          // halves behind one fence, in two boxes a warp, took as long).
 #pragma unroll 1
           for (int bb = 0; bb < 2; ++bb) {
             uint32_t x0[32], x1[32], w[32];
