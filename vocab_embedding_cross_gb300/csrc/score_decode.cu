@@ -26,7 +26,7 @@
 //   T    H     V       K    us      2 V H bytes at
 //   1    2048  151936  20   103     6.0 TB/s (0.88 of the measured copy rate)
 //   1    2048  151936  0    98.6    6.3 TB/s
-//   48   1024  50257   5    28.5    3.6 TB/s
+//   48   1024  50000   5    28.5    3.6 TB/s
 //   128  2048  151936  0    101.5   6.1 TB/s
 // The logits' stores (K > 0) cost 25 us at T = 128. With tiles of 16 KB, a ring
 // whose slots held a share of W and of the tokens each, and the feeding loops in
