@@ -18,12 +18,13 @@
 // each thread's columns are the same for every row, so the weight gradients are
 // summed in its registers over all rows of the group and leave the CTA once, as one
 // partial per CTA (2 H floats for each of at most 152), which a second small kernel
-// adds up: 4 to 6 us behind the first, most of what the backward is above its
-// floor. bf16, warm, in parentheses the share of the measured copy rate:
+// adds up: about 6 us with the partials' way through L2, most of what the backward is
+// above its floor (each further row costs what its bytes cost). bf16, warm, in parentheses the share of the measured copy rate:
 //   forward, RMS     16384 x 2048              22.7 us   5.9 TB/s (0.87)
-//   forward, layer    8192 x 2048              16.0 us
-//   backward, layer   8192 x 2048, fp32 dy     31.0 us   4.3 TB/s (0.64)
-//   backward, layer   8192 x 4096, fp32 dy     49.5 us   5.4 TB/s (0.80)
+//   forward, layer    8192 x 4096              24.0 us   5.6 TB/s (0.82)
+//   backward, layer   8192 x 2048, fp32 dy     30.5 us   4.4 TB/s (0.65)
+//   backward, layer   8192 x 4096, fp32 dy     49.0 us   5.5 TB/s (0.81)
+// One float an instruction instead of two: 26.0, 31.0 and 49.6 us for the last three.
 // Calls of a few rows are bound by the launch (3 us) and the host (6 us a call).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,7 +38,7 @@
 namespace vce {
 namespace {
 
-// 16 bytes of E as floats (8 bf16 or 4 fp32).
+// 16 bytes of E (8 bf16 or 4 fp32) as pairs of floats: two of them an instruction.
 template <typename E>
 struct Row16;
 template <>
@@ -45,14 +46,15 @@ struct Row16<float> {
   static constexpr int N = 4;
   float4 v;
   __device__ __forceinline__ void load(const float* p, int64_t i) { v = reinterpret_cast<const float4*>(p)[i]; }
-  __device__ __forceinline__ void get(float (&f)[4]) const {
-    f[0] = v.x;
-    f[1] = v.y;
-    f[2] = v.z;
-    f[3] = v.w;
+  __device__ __forceinline__ void get(uint64_t (&f)[2]) const {
+    f[0] = pack_f32x2(v.x, v.y);
+    f[1] = pack_f32x2(v.z, v.w);
   }
-  __device__ __forceinline__ static void store(float* p, int64_t i, const float (&f)[4]) {
-    reinterpret_cast<float4*>(p)[i] = make_float4(f[0], f[1], f[2], f[3]);
+  __device__ __forceinline__ static void store(float* p, int64_t i, const uint64_t (&f)[2]) {
+    float4 o;
+    unpack_f32x2(f[0], o.x, o.y);
+    unpack_f32x2(f[1], o.z, o.w);
+    reinterpret_cast<float4*>(p)[i] = o;
   }
 };
 template <>
@@ -60,20 +62,18 @@ struct Row16<__nv_bfloat16> {
   static constexpr int N = 8;
   uint4 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* p, int64_t i) { v = reinterpret_cast<const uint4*>(p)[i]; }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void get(uint64_t (&f)[4]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
+    for (int j = 0; j < 4; ++j) f[j] = pack_f32x2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
   }
-  __device__ __forceinline__ static void store(__nv_bfloat16* p, int64_t i, const float (&f)[8]) {
+  __device__ __forceinline__ static void store(__nv_bfloat16* p, int64_t i, const uint64_t (&f)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      float lo, hi;
+      unpack_f32x2(f[j], lo, hi);
+      w[j] = pack_bf16x2(lo, hi);
     }
     reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -93,17 +93,24 @@ struct RowN {
       for (int j = 0; j < kVecs; ++j) v[j].load(p, i * kVecs + j);
     }
   }
-  __device__ __forceinline__ void get(float (&f)[N]) const {
+  __device__ __forceinline__ void get(uint64_t (&f)[N / 2]) const {
+    constexpr int kPairs = Row16<D>::N / 2;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      float g[Row16<D>::N];
+      uint64_t g[kPairs];
       v[j].get(g);
 #pragma unroll
-      for (int k = 0; k < Row16<D>::N; ++k)
-        if (j * Row16<D>::N + k < N) f[j * Row16<D>::N + k] = g[k];
+      for (int k = 0; k < kPairs; ++k)
+        if (j * kPairs + k < N / 2) f[j * kPairs + k] = g[k];
     }
   }
 };
+__device__ __forceinline__ uint64_t both(float v) { return pack_f32x2(v, v); }
+__device__ __forceinline__ float halves_sum(uint64_t v) {
+  float lo, hi;
+  unpack_f32x2(v, lo, hi);
+  return lo + hi;
+}
 
 // A barrier of one group. Groups of several warps have the named barriers 1 to 15:
 // barrier 0 is the whole CTA's, which another group may already wait at with the
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kFwdThreads)
     norm_fwd_kernel(int64_t T, int H, int G, int slots, const E* __restrict__ x, const E* __restrict__ w,
                     const E* __restrict__ b, float eps, E* __restrict__ y, float* __restrict__ mean,
                     float* __restrict__ rstd, int32_t* status, uint64_t limit_ns) {
-  constexpr int N = Row16<E>::N;
+  constexpr int N = Row16<E>::N, P = N / 2;
   __shared__ float sh[kMaxGroups][64];
   __shared__ uint64_t full[kMaxGroups][kMaxSlots];
   __shared__ int s_abort;
@@ -237,8 +244,8 @@ __global__ void __launch_bounds__(kFwdThreads)
   const float inv = 1.0f / static_cast<float>(H);
   for (; t < T; t += step) {
     const E* row = reinterpret_cast<const E*>(ring.wait());
-    float f[VPT][N];
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, mu = 0.0f;
+    uint64_t f[VPT][P], acc[2] = {0, 0};   // pairs of +0
+    float mu = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (FULL || i0 + j * G < nv) {
@@ -246,35 +253,38 @@ __global__ void __launch_bounds__(kFwdThreads)
         v.load(row, i0 + j * G);
         v.get(f[j]);
 #pragma unroll
-        for (int k = 0; k < N; ++k) acc[k & 3] = RMS ? fmaf(f[j][k], f[j][k], acc[k & 3]) : acc[k & 3] + f[j][k];
+        for (int k = 0; k < P; ++k)
+          acc[k & 1] = RMS ? fma_f32x2(f[j][k], f[j][k], acc[k & 1]) : add_f32x2(acc[k & 1], f[j][k]);
       }
     }
     if (!RMS) {
-      mu = sum((acc[0] + acc[1]) + (acc[2] + acc[3])) * inv;
-      acc[0] = acc[1] = acc[2] = acc[3] = 0.0f;
+      mu = sum(halves_sum(add_f32x2(acc[0], acc[1]))) * inv;
+      acc[0] = acc[1] = 0;
+      const uint64_t less = both(-mu);
 #pragma unroll
       for (int j = 0; j < VPT; ++j)
         if (FULL || i0 + j * G < nv) {
 #pragma unroll
-          for (int k = 0; k < N; ++k) {
-            f[j][k] -= mu;
-            acc[k & 3] = fmaf(f[j][k], f[j][k], acc[k & 3]);
+          for (int k = 0; k < P; ++k) {
+            f[j][k] = add_f32x2(f[j][k], less);
+            acc[k & 1] = fma_f32x2(f[j][k], f[j][k], acc[k & 1]);
           }
         }
     }
-    const float r = __frsqrt_rn(fmaf(sum((acc[0] + acc[1]) + (acc[2] + acc[3])), inv, eps));
+    const float r = __frsqrt_rn(fmaf(sum(halves_sum(add_f32x2(acc[0], acc[1]))), inv, eps));
     __syncwarp();
     fill(ring.slot, t + slots * step);   // the whole group has read the slot
     ring.next();
     E* out = y + t * H;
+    const uint64_t r2 = both(r);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int i = i0 + j * G;
       if (!FULL && i >= nv) continue;
-      float c[N], d[N];
+      uint64_t c[P], d[P];
       Row16<E> v;
 #pragma unroll
-      for (int k = 0; k < N; ++k) f[j][k] *= r;
+      for (int k = 0; k < P; ++k) f[j][k] = mul_f32x2(f[j][k], r2);
       if (w) {
         v.load(reinterpret_cast<const E*>(sw), i);
         v.get(c);
@@ -284,13 +294,13 @@ __global__ void __launch_bounds__(kFwdThreads)
         v.get(d);
       }
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
+      for (int k = 0; k < P; ++k) {
         if (w && b)
-          f[j][k] = fmaf(f[j][k], c[k], d[k]);
+          f[j][k] = fma_f32x2(f[j][k], c[k], d[k]);
         else if (w)
-          f[j][k] *= c[k];
+          f[j][k] = mul_f32x2(f[j][k], c[k]);
         else if (b)
-          f[j][k] += d[k];
+          f[j][k] = add_f32x2(f[j][k], d[k]);
       }
       Row16<E>::store(out, i, f[j]);
     }
@@ -310,7 +320,7 @@ __global__ void __launch_bounds__(kBwdThreads)
     norm_bwd_kernel(int64_t T, int H, int G, int slots, const E* __restrict__ x, const E* __restrict__ w,
                     const D* __restrict__ dy, const float* __restrict__ mean, const float* __restrict__ rstd,
                     E* __restrict__ dx, float* __restrict__ part, int32_t* status, uint64_t limit_ns) {
-  constexpr int N = Row16<E>::N;
+  constexpr int N = Row16<E>::N, P = N / 2;
   __shared__ float sh[kMaxGroups][64];
   __shared__ uint64_t full[kMaxGroups][kMaxSlots];
   __shared__ int s_abort;
@@ -328,12 +338,12 @@ __global__ void __launch_bounds__(kBwdThreads)
   const int warp = i0 >> 5, lane = static_cast<int>(threadIdx.x & 31);
   int buf = 0;
   Row16<E> wv[VPT];
-  float aw[VPT][N], ab[VPT][N];
+  uint64_t aw[VPT][P], ab[VPT][P];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     if (w && (FULL || i0 + j * G < nv)) wv[j].load(w, i0 + j * G);
 #pragma unroll
-    for (int k = 0; k < N; ++k) aw[j][k] = ab[j][k] = 0.0f;
+    for (int k = 0; k < P; ++k) aw[j][k] = ab[j][k] = 0;
   }
   int64_t t = static_cast<int64_t>(blockIdx.x) * groups + g;
   auto fill = [&](int slot, int64_t row) {
@@ -354,13 +364,13 @@ __global__ void __launch_bounds__(kBwdThreads)
   stats(t);
   for (; t < T; t += step) {
     const char* row = ring.wait();
-    float xh[VPT][N], gr[VPT][N];
-    float sg = 0.0f, sx = 0.0f;
+    uint64_t xh[VPT][P], gr[VPT][P], sg2 = 0, sx2 = 0;
     const float rt = r;
+    const uint64_t less = both(-mu), rt2 = both(rt);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (!FULL && i0 + j * G >= nv) continue;
-      float c[N];
+      uint64_t c[P];
       Row16<E> xv;
       RowN<D, N> dv;
       xv.load(reinterpret_cast<const E*>(row), i0 + j * G);
@@ -369,15 +379,16 @@ __global__ void __launch_bounds__(kBwdThreads)
       dv.get(gr[j]);
       if (w) wv[j].get(c);
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        xh[j][k] = (xh[j][k] - mu) * rt;
-        aw[j][k] = fmaf(gr[j][k], xh[j][k], aw[j][k]);
-        ab[j][k] += gr[j][k];
-        if (w) gr[j][k] *= c[k];
-        if (!RMS) sg += gr[j][k];
-        sx = fmaf(gr[j][k], xh[j][k], sx);
+      for (int k = 0; k < P; ++k) {
+        xh[j][k] = mul_f32x2(RMS ? xh[j][k] : add_f32x2(xh[j][k], less), rt2);
+        aw[j][k] = fma_f32x2(gr[j][k], xh[j][k], aw[j][k]);
+        ab[j][k] = add_f32x2(ab[j][k], gr[j][k]);
+        if (w) gr[j][k] = mul_f32x2(gr[j][k], c[k]);
+        if (!RMS) sg2 = add_f32x2(sg2, gr[j][k]);
+        sx2 = fma_f32x2(gr[j][k], xh[j][k], sx2);
       }
     }
+    float sg = halves_sum(sg2), sx = halves_sum(sx2);
     stats(t + step);
     // both sums with one barrier, after which the group has also read the slot
 #pragma unroll
@@ -404,12 +415,13 @@ __global__ void __launch_bounds__(kBwdThreads)
     ring.next();
     if (!dx) continue;
     E* out = dx + t * H;
-    const float mg = RMS ? 0.0f : sg * inv, mx = sx * inv;
+    const uint64_t less_mg = both(-(sg * inv)), less_mx = both(-(sx * inv));
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (!FULL && i0 + j * G >= nv) continue;
 #pragma unroll
-      for (int k = 0; k < N; ++k) gr[j][k] = rt * fmaf(-xh[j][k], mx, RMS ? gr[j][k] : gr[j][k] - mg);
+      for (int k = 0; k < P; ++k)
+        gr[j][k] = mul_f32x2(rt2, fma_f32x2(xh[j][k], less_mx, RMS ? gr[j][k] : add_f32x2(gr[j][k], less_mg)));
       Row16<E>::store(out, i0 + j * G, gr[j]);
     }
   }
@@ -426,11 +438,9 @@ __global__ void __launch_bounds__(kBwdThreads)
       const int i = i0 + j * G;
       if (!FULL && i >= nv) continue;
 #pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        *reinterpret_cast<float4*>(out_part + i * N + k) =
-            make_float4(aw[j][k], aw[j][k + 1], aw[j][k + 2], aw[j][k + 3]);
-        *reinterpret_cast<float4*>(out_part + H + i * N + k) =
-            make_float4(ab[j][k], ab[j][k + 1], ab[j][k + 2], ab[j][k + 3]);
+      for (int k = 0; k < P; k += 2) {   // 16-byte aligned: i * N + 2 k is a multiple of four
+        *reinterpret_cast<ulonglong2*>(out_part + i * N + 2 * k) = make_ulonglong2(aw[j][k], aw[j][k + 1]);
+        *reinterpret_cast<ulonglong2*>(out_part + H + i * N + 2 * k) = make_ulonglong2(ab[j][k], ab[j][k + 1]);
       }
     }
     return;
@@ -444,9 +454,14 @@ __global__ void __launch_bounds__(kBwdThreads)
     const int i = i0 + j * G;
     if (!FULL && i >= nv) continue;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      mine[k * pitch + i] = aw[j][k];
-      mine[region + k * pitch + i] = ab[j][k];
+    for (int k = 0; k < P; ++k) {
+      float lo, hi;
+      unpack_f32x2(aw[j][k], lo, hi);
+      mine[2 * k * pitch + i] = lo;
+      mine[(2 * k + 1) * pitch + i] = hi;
+      unpack_f32x2(ab[j][k], lo, hi);
+      mine[region + 2 * k * pitch + i] = lo;
+      mine[region + (2 * k + 1) * pitch + i] = hi;
     }
   }
   __syncthreads();
