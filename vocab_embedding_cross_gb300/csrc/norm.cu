@@ -19,12 +19,13 @@
 // summed in its registers over all rows of the group and leave the CTA once, as one
 // partial per CTA (2 H floats for each of at most 152), which a second small kernel
 // adds up: about 6 us with the partials' way through L2, most of what the backward is
-// above its floor (each further row costs what its bytes cost). bf16, warm, in parentheses the share of the measured copy rate:
+// above its floor (each further row costs what its bytes cost). bf16, in parentheses
+// the share of the measured copy rate:
 //   forward, RMS     16384 x 2048              22.7 us   5.9 TB/s (0.87)
-//   forward, layer    8192 x 4096              24.0 us   5.6 TB/s (0.82)
-//   backward, layer   8192 x 2048, fp32 dy     30.5 us   4.4 TB/s (0.65)
-//   backward, layer   8192 x 4096, fp32 dy     49.0 us   5.5 TB/s (0.81)
-// One float an instruction instead of two: 26.0, 31.0 and 49.6 us for the last three.
+//   forward, layer    8192 x 4096              24.5 us   5.5 TB/s (0.81)
+//   backward, layer   8192 x 2048, fp32 dy     29.6 us   4.5 TB/s (0.67)
+//   backward, layer   8192 x 4096, fp32 dy     48.6 us   5.5 TB/s (0.81)
+// One float an instruction instead of two: 26.0, 30.3 and 49.6 us for the last three.
 // Calls of a few rows are bound by the launch (3 us) and the host (6 us a call).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -820,7 +821,8 @@ cudaError_t bwd_typed(const vce_problem& p, bool rms, const void* x_, const void
     }
     if (e == cudaSuccess && sums) {
       e = launch_dependent(norm_wide_dw_kernel<E, D>,
-                           dim3(static_cast<unsigned>(ceil_div(H / Row16<E>::N, kColThreads)), static_cast<unsigned>(s.ctas)),
+                           dim3(static_cast<unsigned>(ceil_div(H / Row16<E>::N, kColThreads)),
+                                static_cast<unsigned>(s.ctas)),
                            dim3(kColThreads), 0, st, p.T, H, rms ? 1 : 0, x, dy, mean, rstd, part);
       note_launch(VCE_K_NORM_BWD, st);
     }
