@@ -34,10 +34,10 @@ WORKLOAD = "qwen3_tied"
 # tensor-core kernel's source file that the capture ran: once that file has
 # changed the figure is stale, and the line reports null until it is retaken.
 MEASURED_TRAFFIC = {
-    "qwen3_tied": {"bytes_per_step": 16507500288,
-                   "per_kernel": {"tc_fwd": 793421824, "tc_grad": 3362921216, "tc_dh": 5543381760,
-                                  "tc_dw": 6807775488},
-                   "source": "8394c5a18e8f4645",
+    "qwen3_tied": {"bytes_per_step": 19980925952,
+                   "per_kernel": {"tc_fwd": 849760000, "tc_grad": 3432187904, "tc_dh": 7984088064,
+                                  "tc_dw": 7714889984},
+                   "source": "bf4a39a5a93ac6c4",
                    "profile": "profiles/tc_loss_kernel_qwen3_T8192.md"},
 }
 TC_SOURCE = os.path.join(ROOT, "vocab_embedding_cross_gb300", "csrc", "loss_tc.cu")

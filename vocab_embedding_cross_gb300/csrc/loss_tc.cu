@@ -1569,13 +1569,15 @@ int tc_unit_width(const vce_problem& p) {
 
 int tc_dh_stored_parts(const vce_problem& p) {
   // Where the parts that are added in turn (at most kMaxDhParts a tile) leave
-  // clusters without work: as many as make one wave, each with 16 K blocks or more.
+  // clusters without work: as many as make one wave, each with four K blocks or more
+  // (T = 200, H = 512, V = 3000: 25.9 us the gradient, with 16 or more 30.5; T = 6,
+  // H = 168, V = 4102: 22.4 and 24.7; large vocabularies have more either way).
   const int64_t clusters = current_device_info().num_sms / 2;
   const int64_t tiles = ceil_div(p.T, BMP) * ceil_div(p.H, BN);
   if (tiles * kMaxDhParts >= 2 * clusters) return 1;
   int64_t parts = clusters / tiles;
   const int64_t kb = ceil_div(p.V_real, BK);
-  if (parts > kb / 16) parts = kb / 16;
+  if (parts > kb / 4) parts = kb / 4;
   return parts < 2 ? 1 : static_cast<int>(parts);
 }
 
